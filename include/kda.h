@@ -34,10 +34,11 @@
 #ifndef KDA_H_
 #define KDA_H_
 
-/* 0.3.0: kda_chunk_args ends with `debug_flags`; kda_chunk_fwd_status,
+/* 0.4.0: the operators around the state update added (kda_rms_norm, kda_causal_conv,
+ * kda_gated_scan and their backward and single-token forms). 0.3.0: kda_chunk_args ends with `debug_flags`; kda_chunk_fwd_status,
  * kda_chunk_fwd_noalloc_status and kda_launch_count added. 0.2.0: kda_step_args and kda_token_args
  * end with `state_out` (0.1.0 had no such field). */
-#define KDA_VERSION 300
+#define KDA_VERSION 400
 
 #include <stddef.h>
 #include <stdint.h>
@@ -349,6 +350,268 @@ KDA_API kda_status kda_chunk_fwd_noalloc(const kda_chunk_args *args, void *strea
  * (KDA_ERR_TIMEOUT), or KDA_OK. Calls on other streams since then may have
  * overwritten the word. */
 KDA_API kda_status kda_chunk_fwd_noalloc_status(const kda_chunk_args *args, void *stream);
+
+/*
+ * ---- The operators around the state update of a layer -----------------------
+ * Shared by the entry points below:
+ *  - Activations are rows of channels whose channels are contiguous; `*_stride`
+ *    is the distance between rows in elements (at least the row's length; 0 means
+ *    dense), so a slice of a fused projection is read in place. Outputs are dense.
+ *  - Pointers need the alignment of their element only; rows that are aligned to
+ *    16 bytes (8 bytes for four bf16) with a channel count that is a multiple of
+ *    eight (four for the convolution and the scan) run wider accesses.
+ *  - Packed sequences as in kda_chunk_args: with cu_seqlens B must be 1 and
+ *    cu_seqlens_host, when given, is validated; without it the device copy is
+ *    trusted (it moves no access out of the buffers, whatever it holds).
+ *  - An output that overlaps an input or another output is refused, except where
+ *    stated.
+ *  - Sums, norms, states and convolution windows are fp32.
+ */
+
+/*
+ * Root-mean-square norm of `rows` rows of D channels (1 <= D <= 16384), with the
+ * options that a layer needs:
+ *     s = x (+ residual),  y = s / sqrt(mean(s^2) + eps) * weight * sigmoid(gate)
+ * The gate is the full-rank output gate of page "atlas_core/kimi_k3/kda.rs"
+ * (`full_rank_output_gate`) for whole sequences. The norm is taken of the fp32 sum;
+ * residual_out receives the sum in the activations' dtype.
+ *
+ * With `scales`, y is 8-bit e4m3 (one byte an element) for an 8-bit product: each
+ * row's channels in groups of group_size have scale = max(max|y| / 448, 2^-100) --
+ * with pow2_scales the next power of two -- and hold the nearest e4m3 of y / scale
+ * (a group of zeros has scale 2^-100 and zeros; a NaN in a group makes its scale
+ * NaN).
+ */
+typedef struct {
+    kda_dtype dtype;          /* of x, residual, gate, residual_out, and y without scales */
+    kda_dtype weight_dtype;   /* F32, or dtype */
+    long long rows;
+    int D;
+    const void *x;
+    long long x_stride;
+    const void *residual;     /* NULL: none */
+    long long residual_stride;
+    const void *gate;         /* NULL: none */
+    long long gate_stride;
+    const void *weight;       /* [D], NULL = ones */
+    float eps;                /* >= 0 */
+    void *y;                  /* [rows, D] out */
+    void *residual_out;       /* [rows, D] out, NULL when not wanted; may be `residual` or `x`
+                               * itself (same rows) */
+    float *scales;            /* [rows, ceil(D / group_size)] out: 8-bit output; NULL: y has dtype */
+    int group_size;           /* channels per scale: 32, 64 or 128, 0 = the whole row */
+    int pow2_scales;
+} kda_rms_norm_args;
+
+KDA_API kda_status kda_rms_norm(const kda_rms_norm_args *args, void *stream);
+
+/*
+ * Gradients of kda_rms_norm (without 8-bit output) with respect to s, the gate and
+ * the weight, given dy. x is the normed sum s (the forward's residual_out where a
+ * residual was added), and dx the gradient of both of its terms; dresidual, when
+ * given, is the cotangent of residual_out and is added to it. The weight's gradient
+ * is summed over all rows in a fixed order.
+ */
+typedef struct {
+    kda_dtype dtype;          /* of x, dy, gate, dresidual, dx, dgate */
+    kda_dtype weight_dtype;   /* of weight and dweight: F32, or dtype */
+    long long rows;
+    int D;
+    const void *x;
+    long long x_stride;
+    const void *dy;
+    long long dy_stride;
+    const void *gate;
+    long long gate_stride;
+    const void *dresidual;    /* NULL: none */
+    long long dresidual_stride;
+    const void *weight;
+    float eps;
+    void *dx;                 /* [rows, D] out */
+    void *dgate;              /* [rows, D] out; given exactly when gate is */
+    void *dweight;            /* [D] out, NULL when not wanted (or without weight) */
+    void *workspace;          /* device scratch, 16-byte aligned */
+    size_t workspace_bytes;
+} kda_rms_norm_bwd_args;
+
+/* Bytes of workspace that kda_rms_norm_bwd needs (0 without dweight): shapes and the
+ * presence of dweight are read. */
+KDA_API kda_status kda_rms_norm_bwd_workspace_size(const kda_rms_norm_bwd_args *args, size_t *bytes);
+KDA_API kda_status kda_rms_norm_bwd(const kda_rms_norm_bwd_args *args, void *stream);
+
+/*
+ * Causal depthwise convolution + SiLU over packed sequences: the convolution of
+ * kda_decode_token (page "atlas_core/kimi_k3/kda.rs", `conv_update`) for prompts and
+ * training,
+ *     z[t,c] = sum_k w[c][k] in[t-K+1+k][c],  y = z sigmoid(z)
+ * where each sequence's inputs follow its initial window (the layout of
+ * kda_token_args.conv_state: K values a channel, oldest first; slot 0 has left the
+ * reach of any input). The final window is the last K of window and inputs, so
+ * kda_decode_token and kda_causal_conv_step continue from it.
+ */
+typedef struct {
+    kda_dtype dtype;          /* of x and y */
+    int B, T, C, K;           /* x, y: [B,T,C]; window length K, 1..8 */
+    const void *x;
+    long long x_stride;
+    const float *conv_w;      /* [C, K] fp32 */
+    const float *initial_state; /* [N, C, K] fp32, NULL = zeros */
+    float *final_state;       /* [N, C, K] fp32 out, NULL when not wanted */
+    void *y;
+    const int32_t *cu_seqlens;
+    const int32_t *cu_seqlens_host;
+    int N;
+} kda_conv_args;
+
+KDA_API kda_status kda_causal_conv(const kda_conv_args *args, void *stream);
+
+/* One token of N sequences: the window shifts one slot, x enters the last, and
+ * y = silu(w . window). conv_state is updated IN PLACE. */
+typedef struct {
+    kda_dtype dtype;
+    int N, C, K;
+    const void *x;            /* [N, C] */
+    long long x_stride;
+    const float *conv_w;      /* [C, K] fp32 */
+    float *conv_state;        /* [N, C, K] fp32 */
+    void *y;                  /* [N, C] out */
+} kda_conv_step_args;
+
+KDA_API kda_status kda_causal_conv_step(const kda_conv_step_args *args, void *stream);
+
+/* Gradients of kda_causal_conv given dy and, optionally, the cotangent of the final
+ * windows. dconv_w is summed over all rows in a fixed order. */
+typedef struct {
+    kda_dtype dtype;          /* of x, dy and dx */
+    int B, T, C, K;
+    const void *x;
+    long long x_stride;
+    const void *dy;
+    long long dy_stride;
+    const float *conv_w;
+    const float *initial_state; /* as in the forward */
+    const float *dfinal_state;  /* [N, C, K] or NULL */
+    void *dx;                 /* [B,T,C] out */
+    float *dconv_w;           /* [C, K] out, NULL when not wanted */
+    float *dinitial_state;    /* [N, C, K] out, NULL when not wanted */
+    const int32_t *cu_seqlens;
+    const int32_t *cu_seqlens_host;
+    int N;
+    void *workspace;          /* device scratch, 16-byte aligned */
+    size_t workspace_bytes;
+} kda_conv_bwd_args;
+
+/* Bytes of workspace that kda_causal_conv_bwd needs (0 without dconv_w): shapes and
+ * the presence of dconv_w are read. */
+KDA_API kda_status kda_causal_conv_bwd_workspace_size(const kda_conv_bwd_args *args, size_t *bytes);
+KDA_API kda_status kda_causal_conv_bwd(const kda_conv_bwd_args *args, void *stream);
+
+/*
+ * Gated linear recurrence: the elementwise companion of the chunkwise forward, one
+ * fp32 state a channel, over packed sequences:
+ *     KDA_SCAN_GATE_LOG      a = exp(g) with g clamped below by lower_bound,
+ *                            h_t = a_t h_{t-1} + x_t
+ *     KDA_SCAN_GATE_SIGMOID  a = sigmoid(g) (no lower bound),
+ *                            h_t = a_t h_{t-1} + (1 - a_t) x_t
+ * g <= 0 is expected in the log form (a decay); it is not checked. The state that
+ * the recurrence carries is fp32 throughout, h is rounded as it is written.
+ */
+typedef enum {
+    KDA_SCAN_GATE_LOG = 0,
+    KDA_SCAN_GATE_SIGMOID = 1
+} kda_scan_gate;
+
+typedef struct {
+    kda_dtype dtype;          /* of x, g and h */
+    kda_scan_gate gate;
+    int B, T, D;              /* x, g, h: [B,T,D] */
+    const void *x;
+    long long x_stride;
+    const void *g;
+    long long g_stride;
+    void *h;
+    const float *initial_state; /* [N, D] fp32, NULL = zeros */
+    float *final_state;       /* [N, D] fp32 out, NULL when not wanted */
+    const int32_t *cu_seqlens;
+    const int32_t *cu_seqlens_host;
+    int N;
+    int has_lower_bound;
+    float lower_bound;        /* < 0 */
+    void *workspace;          /* device scratch, 256-byte aligned */
+    size_t workspace_bytes;
+    unsigned int debug_flags; /* 0 in normal use; KDA_DEBUG_STALL_FIRST_WAIT: the first chunk
+                               * of rows does not report, so waits on it give up */
+} kda_scan_args;
+
+/* Bytes of workspace that kda_gated_scan needs (0 where one chunk of rows holds all
+ * sequences). Only shapes and dtype are read. Calls that may overlap on the GPU,
+ * replays of captured graphs among them, need a workspace each. */
+KDA_API kda_status kda_gated_scan_workspace_size(const kda_scan_args *args, size_t *bytes);
+
+/* Queue the recurrence on `stream`. The kernel's CTAs hand states along the rows and
+ * wait for one another with a 2 s limit; a wait that gives up sets the first int32 of
+ * the workspace to 1 (cleared at the start of every call) and lets the kernel finish
+ * with undefined outputs: kda_gated_scan_status reads it. */
+KDA_API kda_status kda_gated_scan(const kda_scan_args *args, void *stream);
+
+/* As kda_chunk_fwd_status: waits for the stream to drain and reports whether a wait of
+ * the last kda_gated_scan with these arguments gave up. */
+KDA_API kda_status kda_gated_scan_status(const kda_scan_args *args, void *stream);
+
+/* One token of N sequences: state <- a state + x (or (1 - a) x), h = state. */
+typedef struct {
+    kda_dtype dtype;
+    kda_scan_gate gate;
+    int N, D;
+    const void *x;            /* [N, D] */
+    long long x_stride;
+    const void *g;
+    long long g_stride;
+    float *state;             /* [N, D] fp32, updated in place unless state_out is given */
+    float *state_out;         /* NULL: in place. Else [N, D] fp32 out, equal to state or not
+                               * overlapping it; state is then only read */
+    void *h;                  /* [N, D] out */
+    int has_lower_bound;
+    float lower_bound;
+} kda_scan_step_args;
+
+KDA_API kda_status kda_gated_scan_step(const kda_scan_step_args *args, void *stream);
+
+/*
+ * Gradients of kda_gated_scan given dout (the cotangent of h) and, optionally, of the
+ * final state. h is the forward's output: h_{t-1} is taken from it as it was rounded
+ * (and from initial_state at a sequence's first row). x is read in the sigmoid form
+ * only. The gradient of g passes where g >= lower_bound, as in kda_chunk_bwd.
+ */
+typedef struct {
+    kda_dtype dtype;          /* of x, g, h, dout, dx, dg */
+    kda_scan_gate gate;
+    int B, T, D;
+    const void *x;            /* NULL allowed in the log form */
+    long long x_stride;
+    const void *g;
+    long long g_stride;
+    const void *h;
+    long long h_stride;
+    const void *dout;
+    long long dout_stride;
+    const float *initial_state; /* as in the forward */
+    const float *dfinal_state;  /* [N, D] or NULL */
+    void *dx, *dg;            /* [B,T,D] out */
+    float *dinitial_state;    /* [N, D] out, NULL when not wanted */
+    const int32_t *cu_seqlens;
+    const int32_t *cu_seqlens_host;
+    int N;
+    int has_lower_bound;
+    float lower_bound;
+    void *workspace;          /* as kda_scan_args */
+    size_t workspace_bytes;
+    unsigned int debug_flags;
+} kda_scan_bwd_args;
+
+KDA_API kda_status kda_gated_scan_bwd_workspace_size(const kda_scan_bwd_args *args, size_t *bytes);
+KDA_API kda_status kda_gated_scan_bwd(const kda_scan_bwd_args *args, void *stream);
+KDA_API kda_status kda_gated_scan_bwd_status(const kda_scan_bwd_args *args, void *stream);
 
 /* Static, human-readable name of a status. */
 KDA_API const char *kda_status_string(kda_status status);

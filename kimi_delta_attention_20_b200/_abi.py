@@ -25,6 +25,9 @@ KDA_GATE_LOG = 0
 KDA_GATE_SOFTPLUS = 1
 KDA_GATE_SAFE = 2
 
+KDA_SCAN_GATE_LOG = 0
+KDA_SCAN_GATE_SIGMOID = 1
+
 KDA_DEBUG_STALL_FIRST_WAIT = 1
 
 _vp = ctypes.c_void_p
@@ -104,11 +107,78 @@ class BwdArgs(ctypes.Structure):
     ]
 
 
+_i, _ll, _f, _sz = ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+_SPAN = [("cu_seqlens", _vp), ("cu_seqlens_host", _vp), ("N", _i)]
+_SCRATCH = [("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+def _rows(*names):
+    """Pointer and row stride of each of the named tensors."""
+    return [f for n in names for f in ((n, _vp), (n + "_stride", _ll))]
+
+
+class RMSNormArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("weight_dtype", _i), ("rows", _ll), ("D", _i), *_rows("x", "residual", "gate"),
+                ("weight", _vp), ("eps", _f), ("y", _vp), ("residual_out", _vp), ("scales", _vp), ("group_size", _i),
+                ("pow2_scales", _i)]
+
+
+class RMSNormBwdArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("weight_dtype", _i), ("rows", _ll), ("D", _i),
+                *_rows("x", "dy", "gate", "dresidual"), ("weight", _vp), ("eps", _f), ("dx", _vp), ("dgate", _vp),
+                ("dweight", _vp), *_SCRATCH]
+
+
+class ConvArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("B", _i), ("T", _i), ("C", _i), ("K", _i), *_rows("x"), ("conv_w", _vp),
+                ("initial_state", _vp), ("final_state", _vp), ("y", _vp), *_SPAN]
+
+
+class ConvStepArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("N", _i), ("C", _i), ("K", _i), *_rows("x"), ("conv_w", _vp), ("conv_state", _vp),
+                ("y", _vp)]
+
+
+class ConvBwdArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("B", _i), ("T", _i), ("C", _i), ("K", _i), *_rows("x", "dy"), ("conv_w", _vp),
+                ("initial_state", _vp), ("dfinal_state", _vp), ("dx", _vp), ("dconv_w", _vp),
+                ("dinitial_state", _vp), *_SPAN, *_SCRATCH]
+
+
+class ScanArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("gate", _i), ("B", _i), ("T", _i), ("D", _i), *_rows("x", "g"), ("h", _vp),
+                ("initial_state", _vp), ("final_state", _vp), *_SPAN, ("has_lower_bound", _i), ("lower_bound", _f),
+                *_SCRATCH, ("debug_flags", ctypes.c_uint)]
+
+
+class ScanStepArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("gate", _i), ("N", _i), ("D", _i), *_rows("x", "g"), ("state", _vp),
+                ("state_out", _vp), ("h", _vp), ("has_lower_bound", _i), ("lower_bound", _f)]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("gate", _i), ("B", _i), ("T", _i), ("D", _i), *_rows("x", "g", "h", "dout"),
+                ("initial_state", _vp), ("dfinal_state", _vp), ("dx", _vp), ("dg", _vp), ("dinitial_state", _vp),
+                *_SPAN, ("has_lower_bound", _i), ("lower_bound", _f), *_SCRATCH, ("debug_flags", ctypes.c_uint)]
+
+
+# entry points of the operators around the state update: name -> argument struct
+_LAYER = {
+    "kda_rms_norm": RMSNormArgs, "kda_rms_norm_bwd": RMSNormBwdArgs, "kda_causal_conv": ConvArgs,
+    "kda_causal_conv_step": ConvStepArgs, "kda_causal_conv_bwd": ConvBwdArgs, "kda_gated_scan": ScanArgs,
+    "kda_gated_scan_status": ScanArgs, "kda_gated_scan_step": ScanStepArgs, "kda_gated_scan_bwd": ScanBwdArgs,
+    "kda_gated_scan_bwd_status": ScanBwdArgs,
+}
+_LAYER_SIZES = {
+    "kda_rms_norm_bwd_workspace_size": RMSNormBwdArgs, "kda_causal_conv_bwd_workspace_size": ConvBwdArgs,
+    "kda_gated_scan_workspace_size": ScanArgs, "kda_gated_scan_bwd_workspace_size": ScanBwdArgs,
+}
+
 # every symbol include/kda.h declares
 EXPORTS = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_chunk_fwd_status",
            "kda_chunk_fwd_noalloc", "kda_chunk_fwd_noalloc_status",
            "kda_recurrent_step", "kda_decode_token", "kda_chunk_bwd_workspace_size", "kda_chunk_bwd",
-           "kda_status_string", "kda_last_cuda_error", "kda_launch_count", "kda_version")
+           "kda_status_string", "kda_last_cuda_error", "kda_launch_count", "kda_version", *_LAYER, *_LAYER_SIZES)
 
 _lib = None
 
@@ -140,6 +210,12 @@ def load():
     lib.kda_chunk_bwd_workspace_size.restype = ctypes.c_int
     lib.kda_chunk_bwd.argtypes = [ctypes.POINTER(BwdArgs), _vp]
     lib.kda_chunk_bwd.restype = ctypes.c_int
+    for name, args in _LAYER.items():
+        getattr(lib, name).argtypes = [ctypes.POINTER(args), _vp]
+        getattr(lib, name).restype = ctypes.c_int
+    for name, args in _LAYER_SIZES.items():
+        getattr(lib, name).argtypes = [ctypes.POINTER(args), ctypes.POINTER(_sz)]
+        getattr(lib, name).restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_cuda_error.argtypes = []

@@ -1,0 +1,555 @@
+"""Python entry points of the operators around the state update of a layer: `rms_norm`,
+`causal_conv` and `chunk_gated_scan`, with their backward and single-token forms.
+
+As in `ops`, PyTorch supplies device memory and the current stream, and every step of the
+computation runs in the library's CUDA kernels. Activations may be slices of a fused
+projection: their channels have to be contiguous and their rows evenly spaced. Outputs are
+contiguous. Each function returns its gradients' counterpart through autograd where an input
+requires grad (the 8-bit norm and the single-token forms have none).
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _abi
+from .ops import _DTYPES, _seqlens
+
+_byref = ctypes.byref
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _need(name, t, device=None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _dtype(name, t):
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return _DTYPES[t.dtype]
+
+
+def _row_stride(t: torch.Tensor):
+    """Distance between the rows (all but the last dimension) of ``t`` in elements, 0 where
+    they are dense; None where the rows are not evenly spaced or their channels are apart."""
+    if t.is_contiguous():
+        return 0
+    shape, stride = t.shape, t.stride()
+    if shape[-1] > 1 and stride[-1] != 1:
+        return None
+    step = None  # of the rows collapsed so far
+    rows = 1
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != step * rows:
+            return None
+        rows *= n
+    if step is None:
+        return 0
+    return step if step >= shape[-1] else None
+
+
+def _act(name, t, like, shape=None):
+    """Row stride of an activation with the dtype and device of ``like``."""
+    _need(name, t, like.device)
+    if t.dtype != like.dtype:
+        raise ValueError(f"{name} must have dtype {like.dtype}")
+    if t.shape != (like.shape if shape is None else shape):
+        raise ValueError(f"{name} must have shape {tuple(like.shape if shape is None else shape)}")
+    stride = _row_stride(t)
+    if stride is None:
+        raise ValueError(f"{name} must have contiguous channels and evenly spaced rows")
+    return stride
+
+
+def _cotangent(name, t, like, shape=None):
+    """A cotangent as autograd hands it over: any strides, brought to dense rows if need be."""
+    _need(name, t, like.device)
+    t = t.to(like.dtype)
+    return t if _row_stride(t) is not None else t.contiguous()
+
+
+def _state(name, t, shape, device):
+    """Pointer of a dense fp32 tensor, or None."""
+    if t is None:
+        return None
+    _need(name, t, device)
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _out(name, t, shape, dtype, device):
+    """The output buffer: the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(name, t, device)
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _launch(fn, a, device, what):
+    if device.index == torch.cuda.current_device():
+        status = fn(_byref(a), torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(_byref(a), torch.cuda.current_stream(device).cuda_stream)
+    if status:
+        _abi.check(status, what)
+
+
+def _scratch(size_fn, a, workspace, device, what):
+    """Gives the call its workspace: the caller's, or a new one where one is needed."""
+    n = ctypes.c_size_t(0)
+    _abi.check(size_fn(_byref(a), _byref(n)), what)
+    if not n.value:
+        return None
+    if workspace is None:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
+    else:
+        _need("workspace", workspace, device)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace  # kept alive by the caller until the launch
+
+
+def _span(x, cu_seqlens, cu_seqlens_cpu, features):
+    """(B, T, N, device offsets, host offsets) of [B, T, channels] activations."""
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B, T, {features}]")
+    B, T = x.shape[:2]
+    if cu_seqlens is None:
+        if cu_seqlens_cpu is not None:
+            raise ValueError("cu_seqlens_cpu needs cu_seqlens")
+        return B, T, B, None, None
+    if B != 1:
+        raise ValueError("cu_seqlens requires B == 1")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must hold N + 1 offsets")
+    if cu_seqlens.is_cuda and cu_seqlens_cpu is None:
+        if cu_seqlens.device != x.device:
+            raise ValueError(f"cu_seqlens must be on {x.device}")
+        dev, host = cu_seqlens.to(torch.int32).contiguous(), None
+    else:
+        dev, host = _seqlens(cu_seqlens, cu_seqlens_cpu, x.device)
+    return B, T, cu_seqlens.numel() - 1, dev, host
+
+
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _no_outs(**outs):
+    for name, t in outs.items():
+        if t is not None:
+            raise ValueError(f"{name} cannot be used when gradients are recorded")
+
+
+# --------------------------------------------------------------------------- RMS norm
+
+def _weight(weight, x):
+    """(pointer, dtype code) of a norm weight."""
+    if weight is None:
+        return None, _abi.KDA_DTYPE_F32
+    _need("weight", weight, x.device)
+    if weight.shape != x.shape[-1:] or weight.dtype not in (torch.float32, x.dtype) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous tensor of {x.shape[-1]} float32 or {x.dtype} values")
+    return weight.data_ptr(), _DTYPES[weight.dtype]
+
+
+def _norm_args(x, weight, residual, gate, eps, residual_out):
+    _need("x", x)
+    dt = _dtype("x", x)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    stride = _act("x", x, x)
+    a = _abi.RMSNormArgs(dtype=dt, rows=rows, D=D, x=_ptr(x), x_stride=stride, eps=eps)
+    a.weight, a.weight_dtype = _weight(weight, x)
+    if residual is not None:
+        a.residual_stride = _act("residual", residual, x)
+        a.residual = _ptr(residual)
+        residual_out = _out("residual_out", residual_out, x.shape, x.dtype, x.device)
+        a.residual_out = _ptr(residual_out)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    if gate is not None:
+        a.gate_stride = _act("gate", gate, x)
+        a.gate = _ptr(gate)
+    return a, residual_out
+
+
+def _rms_norm_fwd(x, weight, residual, gate, eps, out=None, residual_out=None):
+    lib = _abi.load()
+    a, residual_out = _norm_args(x, weight, residual, gate, eps, residual_out)
+    y = _out("out", out, x.shape, x.dtype, x.device)
+    a.y = _ptr(y)
+    _launch(lib.kda_rms_norm, a, x.device, "kda_rms_norm")
+    return y if residual is None else (y, residual_out)
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, gate, eps):
+        r = _rms_norm_fwd(x, weight, residual, gate, eps)
+        ctx.eps = eps
+        ctx.save_for_backward(x if residual is None else r[1], weight, gate)
+        ctx.has_residual = residual is not None
+        return r
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dresidual=None):
+        s, weight, gate = ctx.saved_tensors
+        dx, dgate, dw = rms_norm_bwd(s, dy, weight, gate=gate, dresidual=dresidual, eps=ctx.eps,
+                                     want_dweight=ctx.needs_input_grad[1])
+        return dx, dw, dx if ctx.has_residual else None, dgate, None
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual: Optional[torch.Tensor] = None,
+             gate: Optional[torch.Tensor] = None, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
+             residual_out: Optional[torch.Tensor] = None):
+    """Root-mean-square norm over the last dimension:
+    ``s = x (+ residual)``, ``y = s / sqrt(mean(s^2) + eps) * weight * sigmoid(gate)``.
+
+    x, residual, gate: [..., D] float32 or bfloat16, D up to 16384; weight: [D] float32 or x's
+    dtype, or None. ``gate`` is the output gate of a KDA layer (page
+    "atlas_core/kimi_k3/kda.rs", `full_rank_output_gate`) for whole sequences: x [B, T, H, Dv]
+    is normed per head. Returns y, or with ``residual`` (y, s): the norm is of the float32
+    sum, s is the sum in x's dtype (written to ``residual_out`` if given, which may be
+    ``residual`` or ``x`` itself). Gradients flow to x, weight, residual and gate.
+    """
+    if _wants_grad(x, weight, residual, gate):
+        _no_outs(out=out, residual_out=residual_out)
+        return _RMSNorm.apply(x, weight, residual, gate, eps)
+    return _rms_norm_fwd(x, weight, residual, gate, eps, out, residual_out)
+
+
+def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual: Optional[torch.Tensor] = None,
+                   gate: Optional[torch.Tensor] = None, eps: float = 1e-6, group_size: int = 0,
+                   pow2_scales: bool = False, out: Optional[torch.Tensor] = None,
+                   scales_out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None):
+    """``rms_norm`` with the output in 8 bits for an 8-bit product: (q, scales), or with
+    ``residual`` (q, scales, s), where q [..., D] is float8_e4m3fn and scales [..., groups]
+    float32, y = q * scale. ``group_size`` channels (32, 64 or 128, or 0: the whole row) share
+    the scale max(max|y| / 448, 2^-100), with ``pow2_scales`` rounded up to a power of two.
+    No gradients: inputs that require grad are refused.
+    """
+    if _wants_grad(x, weight, residual, gate):
+        raise NotImplementedError("rms_norm_quant has no gradients; use rms_norm")
+    lib = _abi.load()
+    a, residual_out = _norm_args(x, weight, residual, gate, eps, residual_out)
+    if group_size not in (0, 32, 64, 128):
+        raise ValueError("group_size must be 0 (the whole row), 32, 64 or 128")
+    D = x.shape[-1]
+    groups = -(-D // group_size) if group_size else 1
+    q = _out("out", out, x.shape, torch.float8_e4m3fn, x.device)
+    scales = _out("scales_out", scales_out, (*x.shape[:-1], groups), torch.float32, x.device)
+    a.y, a.scales, a.group_size, a.pow2_scales = _ptr(q), _ptr(scales), group_size, int(pow2_scales)
+    _launch(lib.kda_rms_norm, a, x.device, "kda_rms_norm")
+    return (q, scales) if residual is None else (q, scales, residual_out)
+
+
+def rms_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
+                 gate: Optional[torch.Tensor] = None, dresidual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 want_dweight: bool = True, workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``rms_norm``: (dx, dgate or None, dweight or None) from the cotangent ``dy``
+    of y. x is what was normed: with a residual, the sum s that the forward returned; dx is
+    then the gradient of both terms, and ``dresidual``, the cotangent of s, is added to it.
+    """
+    lib = _abi.load()
+    _need("x", x)
+    dt = _dtype("x", x)
+    dy = _cotangent("dy", dy, x)
+    D = x.shape[-1]
+    a = _abi.RMSNormBwdArgs(dtype=dt, rows=x.numel() // D if D else 0, D=D, x_stride=_act("x", x, x), x=_ptr(x),
+                            dy_stride=_act("dy", dy, x), dy=_ptr(dy), eps=eps)
+    a.weight, a.weight_dtype = _weight(weight, x)
+    dgate = dw = None
+    if gate is not None:
+        a.gate_stride = _act("gate", gate, x)
+        a.gate = _ptr(gate)
+        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        a.dgate = _ptr(dgate)
+    if dresidual is not None:
+        dresidual = _cotangent("dresidual", dresidual, x)
+        a.dresidual_stride = _act("dresidual", dresidual, x)
+        a.dresidual = _ptr(dresidual)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a.dx = _ptr(dx)
+    if weight is not None and want_dweight:
+        dw = torch.empty_like(weight)
+        a.dweight = _ptr(dw)
+    ws = _scratch(lib.kda_rms_norm_bwd_workspace_size, a, workspace, x.device, "kda_rms_norm_bwd_workspace_size")  # noqa: F841
+    _launch(lib.kda_rms_norm_bwd, a, x.device, "kda_rms_norm_bwd")
+    return dx, dgate, dw
+
+
+# --------------------------------------------------------------------------- causal convolution
+
+def _conv_weight(conv_w, x):
+    _need("conv_w", conv_w, x.device)
+    if conv_w.dtype != torch.float32 or conv_w.dim() != 2 or conv_w.shape[0] != x.shape[-1] or not conv_w.is_contiguous():
+        raise ValueError(f"conv_w must be a contiguous float32 tensor [{x.shape[-1]}, K]")
+    return conv_w.shape[1]
+
+
+def _causal_conv_fwd(x, conv_w, initial_state, want_final, cu_seqlens, cu_seqlens_cpu, out=None, final_state_out=None):
+    lib = _abi.load()
+    _need("x", x)
+    dt = _dtype("x", x)
+    B, T, N, cu, cu_host = _span(x, cu_seqlens, cu_seqlens_cpu, "C")
+    C, K = x.shape[2], _conv_weight(conv_w, x)
+    stride = _act("x", x, x)
+    s0 = _state("initial_state", initial_state, (N, C, K), x.device)
+    y = _out("out", out, x.shape, x.dtype, x.device)
+    fs = _out("final_state_out", final_state_out, (N, C, K), torch.float32, x.device) if want_final else None
+    a = _abi.ConvArgs(dt, B, T, C, K, _ptr(x), stride, conv_w.data_ptr(), s0, _ptr(fs), _ptr(y), _ptr(cu), _ptr(cu_host), N)
+    _launch(lib.kda_causal_conv, a, x.device, "kda_causal_conv")
+    return y, fs, cu, cu_host
+
+
+class _CausalConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, conv_w, initial_state, want_final, cu_seqlens, cu_seqlens_cpu):
+        y, fs, cu, cu_host = _causal_conv_fwd(x, conv_w, initial_state, want_final, cu_seqlens, cu_seqlens_cpu)
+        ctx.save_for_backward(x, conv_w, initial_state)
+        ctx.cu = cu, cu_host
+        ctx.set_materialize_grads(False)
+        return y, fs
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dfs):
+        x, conv_w, s0 = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        dx, dw, ds0 = causal_conv_bwd(
+            x, conv_w, dy, initial_state=s0, dfinal_state=dfs, cu_seqlens=ctx.cu[0], cu_seqlens_cpu=ctx.cu[1],
+            want_dconv_w=ctx.needs_input_grad[1], want_dinitial_state=s0 is not None and ctx.needs_input_grad[2])
+        return dx, dw, ds0, None, None, None
+
+
+def causal_conv(x: torch.Tensor, conv_w: torch.Tensor, *, initial_state: Optional[torch.Tensor] = None,
+                output_final_state: bool = False, cu_seqlens: Optional[torch.Tensor] = None,
+                cu_seqlens_cpu: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                final_state_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Causal depthwise convolution + SiLU over whole sequences: the convolution of
+    ``decode_token`` for prompts and training (page "atlas_core/kimi_k3/kda.rs", `conv_update`).
+
+    x: [B, T, C] float32 or bfloat16; conv_w: [C, K] float32, K in 1..8, oldest tap first;
+    initial_state: [N, C, K] float32 windows in the layout of ``decode_token``'s conv_state
+    (None: zeros). ``cu_seqlens`` (int32, [N+1], B == 1) packs N sequences, on the CPU or, for
+    calls that are captured or must not wait, on the device; ``cu_seqlens_cpu``, its host copy,
+    is validated when given. Returns (y [B, T, C], final windows [N, C, K] or None);
+    ``decode_token`` and ``causal_conv_step`` continue from the windows. Gradients flow to x,
+    conv_w and initial_state.
+    """
+    if _wants_grad(x, conv_w, initial_state):
+        _no_outs(out=out, final_state_out=final_state_out)
+        return _CausalConv.apply(x, conv_w, initial_state, output_final_state, cu_seqlens, cu_seqlens_cpu)
+    return _causal_conv_fwd(x, conv_w, initial_state, output_final_state, cu_seqlens, cu_seqlens_cpu, out, final_state_out)[:2]
+
+
+def causal_conv_step(x: torch.Tensor, conv_w: torch.Tensor, conv_state: torch.Tensor, *,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of N sequences: x [N, C], conv_w [C, K] float32, conv_state [N, C, K] float32,
+    updated IN PLACE (shifted one slot, x last). Returns silu(w . window) [N, C].
+    """
+    lib = _abi.load()
+    _need("x", x)
+    dt = _dtype("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C]")
+    N, C = x.shape
+    K = _conv_weight(conv_w, x)
+    stride = _act("x", x, x)
+    s = _state("conv_state", conv_state, (N, C, K), x.device)
+    y = _out("out", out, x.shape, x.dtype, x.device)
+    a = _abi.ConvStepArgs(dt, N, C, K, _ptr(x), stride, conv_w.data_ptr(), s, _ptr(y))
+    _launch(lib.kda_causal_conv_step, a, x.device, "kda_causal_conv_step")
+    return y
+
+
+def causal_conv_bwd(x: torch.Tensor, conv_w: torch.Tensor, dy: torch.Tensor, *,
+                    initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                    cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_cpu: Optional[torch.Tensor] = None,
+                    want_dconv_w: bool = True, want_dinitial_state: Optional[bool] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``causal_conv``: (dx, dconv_w or None, dinitial_state or None) from the
+    cotangents ``dy`` of y and, optionally, ``dfinal_state`` [N, C, K] float32 of the final
+    windows. dinitial_state comes with an initial_state unless asked for otherwise.
+    """
+    lib = _abi.load()
+    _need("x", x)
+    dt = _dtype("x", x)
+    B, T, N, cu, cu_host = _span(x, cu_seqlens, cu_seqlens_cpu, "C")
+    C, K = x.shape[2], _conv_weight(conv_w, x)
+    dy = _cotangent("dy", dy, x)
+    if dfinal_state is not None:
+        dfinal_state = dfinal_state.contiguous()
+    if want_dinitial_state is None:
+        want_dinitial_state = initial_state is not None
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(conv_w) if want_dconv_w else None
+    ds0 = torch.empty((N, C, K), dtype=torch.float32, device=x.device) if want_dinitial_state else None
+    a = _abi.ConvBwdArgs(dt, B, T, C, K, _ptr(x), _act("x", x, x), _ptr(dy), _act("dy", dy, x), conv_w.data_ptr(),
+                         _state("initial_state", initial_state, (N, C, K), x.device),
+                         _state("dfinal_state", dfinal_state, (N, C, K), x.device), _ptr(dx), _ptr(dw), _ptr(ds0),
+                         _ptr(cu), _ptr(cu_host), N)
+    ws = _scratch(lib.kda_causal_conv_bwd_workspace_size, a, workspace, x.device, "kda_causal_conv_bwd_workspace_size")  # noqa: F841
+    _launch(lib.kda_causal_conv_bwd, a, x.device, "kda_causal_conv_bwd")
+    return dx, dw, ds0
+
+
+# --------------------------------------------------------------------------- gated scan
+
+def _scan_gate(sigmoid, lower_bound):
+    """(gate form, has bound, bound)"""
+    if lower_bound is None:
+        return (_abi.KDA_SCAN_GATE_SIGMOID if sigmoid else _abi.KDA_SCAN_GATE_LOG), 0, 0.0
+    if sigmoid:
+        raise ValueError("lower_bound applies to the log-decay form only")
+    if not lower_bound < 0:
+        raise ValueError("lower_bound must be negative")
+    return _abi.KDA_SCAN_GATE_LOG, 1, float(lower_bound)
+
+
+def _gated_scan_fwd(x, g, initial_state, want_final, sigmoid, lower_bound, cu_seqlens, cu_seqlens_cpu, out=None,
+                    final_state_out=None, workspace=None):
+    lib = _abi.load()
+    _need("x", x)
+    dt = _dtype("x", x)
+    gate, has_lb, lb = _scan_gate(sigmoid, lower_bound)
+    B, T, N, cu, cu_host = _span(x, cu_seqlens, cu_seqlens_cpu, "D")
+    D = x.shape[2]
+    xs, gs = _act("x", x, x), _act("g", g, x)
+    s0 = _state("initial_state", initial_state, (N, D), x.device)
+    h = _out("out", out, x.shape, x.dtype, x.device)
+    fs = _out("final_state_out", final_state_out, (N, D), torch.float32, x.device) if want_final else None
+    a = _abi.ScanArgs(dt, gate, B, T, D, _ptr(x), xs, _ptr(g), gs, _ptr(h), s0, _ptr(fs), _ptr(cu), _ptr(cu_host), N,
+                      has_lb, lb)
+    ws = _scratch(lib.kda_gated_scan_workspace_size, a, workspace, x.device, "kda_gated_scan_workspace_size")  # noqa: F841
+    _launch(lib.kda_gated_scan, a, x.device, "kda_gated_scan")
+    return h, fs, cu, cu_host
+
+
+class _GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, initial_state, want_final, sigmoid, lower_bound, cu_seqlens, cu_seqlens_cpu):
+        h, fs, cu, cu_host = _gated_scan_fwd(x, g, initial_state, want_final, sigmoid, lower_bound, cu_seqlens, cu_seqlens_cpu)
+        ctx.save_for_backward(x if sigmoid else None, g, h, initial_state)
+        ctx.gate, ctx.cu = (sigmoid, lower_bound), (cu, cu_host)
+        ctx.set_materialize_grads(False)
+        return h, fs
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh, dfs):
+        x, g, h, s0 = ctx.saved_tensors
+        if dh is None:
+            dh = torch.zeros(h.shape, dtype=h.dtype, device=h.device)
+        dx, dg, ds0 = chunk_gated_scan_bwd(
+            x, g, h, dh, initial_state=s0, dfinal_state=dfs, use_gate_sigmoid_in_kernel=ctx.gate[0],
+            lower_bound=ctx.gate[1], cu_seqlens=ctx.cu[0], cu_seqlens_cpu=ctx.cu[1],
+            want_dinitial_state=s0 is not None and ctx.needs_input_grad[2])
+        return dx, dg, ds0, None, None, None, None, None
+
+
+def chunk_gated_scan(x: torch.Tensor, g: torch.Tensor, *, initial_state: Optional[torch.Tensor] = None,
+                     output_final_state: bool = False, use_gate_sigmoid_in_kernel: bool = False,
+                     lower_bound: Optional[float] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                     cu_seqlens_cpu: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     final_state_out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Gated linear recurrence per channel over whole sequences, the elementwise companion of
+    ``chunk_kda``: ``h_t = a_t h_{t-1} + x_t``, with ``a = exp(max(g, lower_bound))`` of the
+    log-decay g (<= 0); or, with ``use_gate_sigmoid_in_kernel``, of the gate's logit g
+    ``a = sigmoid(g)`` and ``h_t = a_t h_{t-1} + (1 - a_t) x_t``.
+
+    x, g: [B, T, D] float32 or bfloat16; initial_state: [N, D] float32 (None: zeros).
+    ``cu_seqlens`` as in ``causal_conv``. The state is carried in float32; h is rounded to x's
+    dtype as it is written. Returns (h [B, T, D], final state [N, D] float32 or None).
+    Gradients flow to x, g and initial_state. A ``workspace`` passed in belongs to one call at
+    a time (captured graphs that may overlap need one each).
+    """
+    if _wants_grad(x, g, initial_state):
+        _no_outs(out=out, final_state_out=final_state_out, workspace=workspace)
+        return _GatedScan.apply(x, g, initial_state, output_final_state, use_gate_sigmoid_in_kernel, lower_bound,
+                                cu_seqlens, cu_seqlens_cpu)
+    return _gated_scan_fwd(x, g, initial_state, output_final_state, use_gate_sigmoid_in_kernel, lower_bound, cu_seqlens,
+                           cu_seqlens_cpu, out, final_state_out, workspace)[:2]
+
+
+def gated_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *, use_gate_sigmoid_in_kernel: bool = False,
+                    lower_bound: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    state_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of N sequences: x, g [N, D]; state [N, D] float32, updated IN PLACE, or only
+    read when ``state_out`` (a second buffer, disjoint from it) receives the new state. Gate
+    arguments as in ``chunk_gated_scan``. Returns h [N, D].
+    """
+    lib = _abi.load()
+    _need("x", x)
+    dt = _dtype("x", x)
+    gate, has_lb, lb = _scan_gate(use_gate_sigmoid_in_kernel, lower_bound)
+    if x.dim() != 2:
+        raise ValueError("x must be [N, D]")
+    xs, gs = _act("x", x, x), _act("g", g, x)
+    s, so = _state("state", state, x.shape, x.device), _state("state_out", state_out, x.shape, x.device)
+    h = _out("out", out, x.shape, x.dtype, x.device)
+    a = _abi.ScanStepArgs(dt, gate, x.shape[0], x.shape[1], _ptr(x), xs, _ptr(g), gs, s, so, _ptr(h), has_lb, lb)
+    _launch(lib.kda_gated_scan_step, a, x.device, "kda_gated_scan_step")
+    return h
+
+
+def chunk_gated_scan_bwd(x: Optional[torch.Tensor], g: torch.Tensor, h: torch.Tensor, dout: torch.Tensor, *,
+                         initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                         use_gate_sigmoid_in_kernel: bool = False, lower_bound: Optional[float] = None,
+                         cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_cpu: Optional[torch.Tensor] = None,
+                         want_dinitial_state: Optional[bool] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``chunk_gated_scan``: (dx, dg, dinitial_state or None) from the cotangents
+    ``dout`` of h and, optionally, ``dfinal_state`` [N, D] float32. h is the forward's output;
+    x is needed with ``use_gate_sigmoid_in_kernel`` only (None otherwise). dg is zero where
+    the lower bound is taken (g < lower_bound). dinitial_state comes with an initial_state
+    unless asked for otherwise.
+    """
+    lib = _abi.load()
+    _need("g", g)
+    dt = _dtype("g", g)
+    gate, has_lb, lb = _scan_gate(use_gate_sigmoid_in_kernel, lower_bound)
+    if use_gate_sigmoid_in_kernel and x is None:
+        raise ValueError("x is required with use_gate_sigmoid_in_kernel")
+    if not use_gate_sigmoid_in_kernel:
+        x = None
+    B, T, N, cu, cu_host = _span(g, cu_seqlens, cu_seqlens_cpu, "D")
+    D = g.shape[2]
+    dout = _cotangent("dout", dout, g)
+    if dfinal_state is not None:
+        dfinal_state = dfinal_state.contiguous()
+    if want_dinitial_state is None:
+        want_dinitial_state = initial_state is not None
+    dx, dg = (torch.empty(g.shape, dtype=g.dtype, device=g.device) for _ in range(2))
+    ds0 = torch.empty((N, D), dtype=torch.float32, device=g.device) if want_dinitial_state else None
+    a = _abi.ScanBwdArgs(dt, gate, B, T, D, _ptr(x), 0 if x is None else _act("x", x, g), _ptr(g), _act("g", g, g),
+                         _ptr(h), _act("h", h, g), _ptr(dout), _act("dout", dout, g),
+                         _state("initial_state", initial_state, (N, D), g.device),
+                         _state("dfinal_state", dfinal_state, (N, D), g.device), _ptr(dx), _ptr(dg), _ptr(ds0), _ptr(cu),
+                         _ptr(cu_host), N, has_lb, lb)
+    ws = _scratch(lib.kda_gated_scan_bwd_workspace_size, a, workspace, g.device, "kda_gated_scan_bwd_workspace_size")  # noqa: F841
+    _launch(lib.kda_gated_scan_bwd, a, g.device, "kda_gated_scan_bwd")
+    return dx, dg, ds0
