@@ -537,26 +537,19 @@ typedef struct {
     int N;
     int has_lower_bound;
     float lower_bound;        /* < 0 */
-    void *workspace;          /* device scratch, 256-byte aligned */
+    void *workspace;          /* device scratch, 16-byte aligned */
     size_t workspace_bytes;
-    unsigned int debug_flags; /* 0 in normal use; KDA_DEBUG_STALL_FIRST_WAIT: the first chunk
-                               * of rows does not report, so waits on it give up */
 } kda_scan_args;
 
-/* Bytes of workspace that kda_gated_scan needs (0 where one chunk of rows holds all
- * sequences). Only shapes and dtype are read. Calls that may overlap on the GPU,
- * replays of captured graphs among them, need a workspace each. */
+/* Bytes of workspace that kda_gated_scan needs (0 where no sequence is cut along time).
+ * Shapes, dtype and the offsets (cu_seqlens_host, and whether cu_seqlens is given) are
+ * read. Calls that may overlap on the GPU, replays of captured graphs among them, need a
+ * workspace each. */
 KDA_API kda_status kda_gated_scan_workspace_size(const kda_scan_args *args, size_t *bytes);
 
-/* Queue the recurrence on `stream`. The kernel's CTAs hand states along the rows and
- * wait for one another with a 2 s limit; a wait that gives up sets the first int32 of
- * the workspace to 1 (cleared at the start of every call) and lets the kernel finish
- * with undefined outputs: kda_gated_scan_status reads it. */
+/* Queue the recurrence on `stream`: one launch, or two where sequences are cut along time
+ * to fill the GPU (results depend on the shapes alone, not on timing). */
 KDA_API kda_status kda_gated_scan(const kda_scan_args *args, void *stream);
-
-/* As kda_chunk_fwd_status: waits for the stream to drain and reports whether a wait of
- * the last kda_gated_scan with these arguments gave up. */
-KDA_API kda_status kda_gated_scan_status(const kda_scan_args *args, void *stream);
 
 /* One token of N sequences: state <- a state + x (or (1 - a) x), h = state. */
 typedef struct {
@@ -606,12 +599,10 @@ typedef struct {
     float lower_bound;
     void *workspace;          /* as kda_scan_args */
     size_t workspace_bytes;
-    unsigned int debug_flags;
 } kda_scan_bwd_args;
 
 KDA_API kda_status kda_gated_scan_bwd_workspace_size(const kda_scan_bwd_args *args, size_t *bytes);
 KDA_API kda_status kda_gated_scan_bwd(const kda_scan_bwd_args *args, void *stream);
-KDA_API kda_status kda_gated_scan_bwd_status(const kda_scan_bwd_args *args, void *stream);
 
 /* Static, human-readable name of a status. */
 KDA_API const char *kda_status_string(kda_status status);

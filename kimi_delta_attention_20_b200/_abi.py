@@ -148,7 +148,7 @@ class ConvBwdArgs(ctypes.Structure):
 class ScanArgs(ctypes.Structure):
     _fields_ = [("dtype", _i), ("gate", _i), ("B", _i), ("T", _i), ("D", _i), *_rows("x", "g"), ("h", _vp),
                 ("initial_state", _vp), ("final_state", _vp), *_SPAN, ("has_lower_bound", _i), ("lower_bound", _f),
-                *_SCRATCH, ("debug_flags", ctypes.c_uint)]
+                *_SCRATCH]
 
 
 class ScanStepArgs(ctypes.Structure):
@@ -159,15 +159,14 @@ class ScanStepArgs(ctypes.Structure):
 class ScanBwdArgs(ctypes.Structure):
     _fields_ = [("dtype", _i), ("gate", _i), ("B", _i), ("T", _i), ("D", _i), *_rows("x", "g", "h", "dout"),
                 ("initial_state", _vp), ("dfinal_state", _vp), ("dx", _vp), ("dg", _vp), ("dinitial_state", _vp),
-                *_SPAN, ("has_lower_bound", _i), ("lower_bound", _f), *_SCRATCH, ("debug_flags", ctypes.c_uint)]
+                *_SPAN, ("has_lower_bound", _i), ("lower_bound", _f), *_SCRATCH]
 
 
 # entry points of the operators around the state update: name -> argument struct
 _LAYER = {
     "kda_rms_norm": RMSNormArgs, "kda_rms_norm_bwd": RMSNormBwdArgs, "kda_causal_conv": ConvArgs,
     "kda_causal_conv_step": ConvStepArgs, "kda_causal_conv_bwd": ConvBwdArgs, "kda_gated_scan": ScanArgs,
-    "kda_gated_scan_status": ScanArgs, "kda_gated_scan_step": ScanStepArgs, "kda_gated_scan_bwd": ScanBwdArgs,
-    "kda_gated_scan_bwd_status": ScanBwdArgs,
+    "kda_gated_scan_step": ScanStepArgs, "kda_gated_scan_bwd": ScanBwdArgs,
 }
 _LAYER_SIZES = {
     "kda_rms_norm_bwd_workspace_size": RMSNormBwdArgs, "kda_causal_conv_bwd_workspace_size": ConvBwdArgs,

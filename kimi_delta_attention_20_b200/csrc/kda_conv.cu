@@ -5,266 +5,290 @@
 // where a sequence's inputs are preceded by its initial window (K values a channel, oldest
 // first, or zeros), and its final window is the last K of both.
 //
-// Bound by HBM: 4 bytes an element forward, 6 backward (bf16). A warp takes S consecutive
-// rows of 128 channels, four a lane, and slides the window down them in registers; the
-// K - 1 rows before its own are read again (from L1 or L2: the neighbouring warp's rows).
+// Bound by HBM: 4 bytes an element forward, 6 backward (bf16). A walker slides the window
+// down its piece of the rows in registers. Nothing is carried between pieces but K - 1
+// rows that are read twice, so pieces are cut for full waves of walkers: twelve an SM with
+// rings of 16 KiB, since the backward needs the arithmetic of many warps beside the bytes
+// in flight.
 #include "kda_layer.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int kConvWarps = 8, kConvThreads = 32 * kConvWarps;
-constexpr int kConvRows = 16;  // rows of a warp
+constexpr int kConvSlots = 148 * 12;  // walkers that run at the same time
+constexpr int kMinPiece = 32;         // rows of a piece, at least
+template <typename T, bool AL> using FwdRing = Ring<T, AL, 1, 8>;
+template <typename T, bool AL> using BwdRing = Ring<T, AL, 2, 4>;
 
-__device__ __forceinline__ float silu_(float z) { return z / (1.f + expf(-z)); }
-
-// The sequence that row `first + at` of the map belongs to, and its first row.
-template <int L>
-__device__ __forceinline__ void sequence_at(const RowMap<L> &m, int row0, int at, int lane, int &seq, int &start) {
-    seq = m.first_seq;
-    start = m.first;
-    for (int b = at & ~31; b >= 0; b -= 32) {
-        const int r = b + lane;
-        const unsigned hit = __ballot_sync(0xffffffffu, r <= at && m.start[r] >= 0);
-        if (hit) {
-            const int s = b + 31 - __clz(hit);
-            seq = m.start[s];
-            start = row0 + s;
-            return;
-        }
-    }
+// sigmoid, by the SFU where the result is rounded to bf16.
+template <typename T> __device__ __forceinline__ float sig(float z) {
+    return sizeof(T) == 2 ? rcp_fast(1.f + ex2_fast(-kLog2e * z)) : 1.f / (1.f + expf(-z));
 }
 
-// The lane's weights: w[c, 0..K-1] of its four channels.
-template <bool VEC, int K>
-__device__ __forceinline__ void load_weights(const float *w, int tile, int lane, int C, float (&wr)[K][4]) {
+// The lane's weights: w[c, 0..K-1] of its channels.
+template <int K, int W> __device__ __forceinline__ void load_weights(const float *w, int c, int C, float (&wr)[K][W]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = lane_channel<VEC>(tile, lane, i);
+    for (int i = 0; i < W; ++i)
 #pragma unroll
-        for (int k = 0; k < K; ++k) wr[k][i] = c < C ? w[(long long)c * K + k] : 0.f;
-    }
+        for (int k = 0; k < K; ++k) wr[k][i] = c + i < C ? w[(long long)(c + i) * K + k] : 0.f;
 }
 
-// Slot k of sequence n's initial window (zeros where there is none).
-template <bool VEC>
-__device__ __forceinline__ void window_slot(const float *s0, int n, int k, int K, int tile, int lane, int C, float (&v)[4]) {
+// Slot k of sequence n's window (zeros where there is none).
+template <int W> __device__ __forceinline__ void window_slot(const float *s0, int n, int k, int K, int c, int C, float (&v)[W]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = lane_channel<VEC>(tile, lane, i);
-        v[i] = s0 && c < C ? s0[((long long)n * C + c) * K + k] : 0.f;
-    }
+    for (int i = 0; i < W; ++i) v[i] = s0 && c + i < C ? s0[((long long)n * C + c + i) * K + k] : 0.f;
 }
 
-// win[0..K-2]: the K - 1 inputs before `row` of a sequence that starts at `start`.
-template <typename T, bool VEC, int K>
-__device__ __forceinline__ void load_window(const T *x, long long stride, const float *s0, int row, int seq, int start,
-                                            int tile, int lane, int C, float (&win)[K][4]) {
+// win[0..K-2]: the K - 1 inputs before `row` of sequence q.
+template <typename T, int K, int W>
+__device__ __forceinline__ void load_window(const T *x, long long stride, const float *s0, int row, const Seq &q, int c, int C, float (&win)[K][W]) {
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) {
         const int r = row - (K - 1) + k;
-        if (r >= start) {
-            const Raw4<T> q = load_row<T, VEC>(x + (long long)r * stride, tile, lane, C, true);
+        if (r >= q.start) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) win[k][i] = raw_get(q, i);
+            for (int i = 0; i < W; ++i) win[k][i] = c + i < C ? to_f32(x[r * stride + c + i]) : 0.f;
         } else {
             // inputs `start - r` before the sequence's first sit that far from the window's end
-            const int slot = K - (start - r);
-            if (slot >= 0) window_slot<VEC>(s0, seq, slot, K, tile, lane, C, win[k]);
-            else win[k][0] = win[k][1] = win[k][2] = win[k][3] = 0.f;
+            window_slot(s0, q.n, K - (q.start - r), K, c, C, win[k]);
         }
     }
 }
 
-// ---------------------------------------------------------------- forward
-template <typename T, bool VEC, int K>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(const __grid_constant__ ConvParams p) {
-    constexpr int S = kConvRows, L = kConvWarps * S;
-    __shared__ RowMap<L> map;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tiles = (p.C + kTileChannels - 1) / kTileChannels, block = blockIdx.x / tiles;
-    const int tile = blockIdx.x - block * tiles, row0 = block * L, wrow = row0 + warp * S, R = p.span.R, C = p.C;
-    const T *x = static_cast<const T *>(p.x);
+// win <- its rotation by n: slot k becomes slot (k - n) mod K.
+template <int K, int W> __device__ __forceinline__ void rotate(float (&win)[K][W], int n) {
+    float t[K][W];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) t[k][i] = win[(k + n) % K][i];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < W; ++i) win[k][i] = t[k][i];
+}
 
-    Raw4<T> xr[S];
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-        xr[s] = load_row<T, VEC>(x + (long long)(wrow + s) * p.x_stride, tile, lane, C, wrow + s < R);
-    float w[K][4];
-    load_weights<VEC, K>(p.w, tile, lane, C, w);
+// ---------------------------------------------------------------- forward
+template <typename T, bool AL, int K>
+__global__ void __launch_bounds__(32) conv_fwd_kernel(const __grid_constant__ ConvParams p) {
+    using RN = FwdRing<T, AL>;
+    constexpr int W = RN::W, S = kStageRows, ST = 8, TC = walk_channels<T>();
+    extern __shared__ __align__(16) char dyn[];
+    const int lane = threadIdx.x, C = p.C, R = p.span.R, units = (C + TC - 1) / TC;
+    const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
+    const int b = min(piece * p.piece, R), e = piece + 1 == p.pieces ? R : min(b + p.piece, R);
+    const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R)}, min(TC, C - c0) * (int)sizeof(T), lane};
+#pragma unroll 1
+    for (int k = 0; k < ST - 1; ++k) {
+        if (b + k * S < e) ring.load(k, 0, b + k * S, b, e);
+        cp_async_commit();
+    }
+    float w[K][W];
+    load_weights<K, W>(p.w, c, C, w);
     // an empty sequence hands its window through
-    fill_rows<L>(map, p.span, row0, [&](int n) {
-        if (!p.sT) return;
-        const long long c0 = ((long long)n * C + tile * kTileChannels) * K, c1 = ((long long)n * C + min(C, (tile + 1) * kTileChannels)) * K;
-        for (long long c = c0; c < c1; ++c) p.sT[c] = p.s0 ? p.s0[c] : 0.f;
-    });
-    if (wrow >= R) return;
-    float win[K][4];  // win[K-1]: the row's own input
-    int seq, start;
-    sequence_at<L>(map, row0, warp * S, lane, seq, start);
-    load_window<T, VEC, K>(x, p.x_stride, p.s0, wrow, seq, start, tile, lane, C, win);
+    hand_through<W>(p.span, piece, p.pieces, lane, c, C, K, p.sT, p.s0);
+    if (b >= e) return;
+    Seq q = seq_of(p.span, b, lane);
+    float win[K][W];  // at the s-th row of a stage slot (s + k) % K is input s + k - (K - 1)
+    load_window<T, K, W>(static_cast<const T *>(p.x), p.x_stride, p.s0, b, q, c, C, win);
+    T *y = static_cast<T *>(p.y) + (long long)b * C;
+    int slot = 0, next = ST - 1;
+#pragma unroll 1
+    for (int r = b; r < e; r += S) {
+        cp_async_wait_group<ST - 2>();
+        __syncwarp();
+        const int ahead = r + (ST - 1) * S;
+        if (ahead < e) ring.load(next, 0, ahead, b, e);
+        cp_async_commit();
+        // row r + s with the window's oldest input in slot j
+        auto one = [&](int s, int j) {
+            float z[W];
+            ring.get(slot, 0, s, r + s, win[(j + K - 1) % K]);
+            vmul(w[0], win[j % K], z);
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-        const int row = wrow + s;
-        if (row < R) {
-            if (s > 0 && map.start[warp * S + s] >= 0) {
-                seq = map.start[warp * S + s];
+            for (int k = 1; k < K; ++k) vfma(w[k], win[(j + k) % K], z, z);
 #pragma unroll
-                for (int k = 0; k < K - 1; ++k) window_slot<VEC>(p.s0, seq, k + 1, K, tile, lane, C, win[k]);
+            for (int i = 0; i < W; ++i) z[i] *= sig<T>(z[i]);
+            put_row<AL>(y + (long long)s * C, c, C, lane, z);
+        };
+        // behind the last row of a sequence, its last K inputs in slots j, j + 1 ..
+        auto close = [&](int row, int j) {
+            if (p.sT) {
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        if (c + i < C) p.sT[((long long)q.n * C + c + i) * K + k] = win[(j + k) % K][i];
             }
-            float y[4];
+            if (row < e) {
+                q = seq_of(p.span, row, lane);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                win[K - 1][i] = raw_get(xr[s], i);
-                float z = 0.f;
-#pragma unroll
-                for (int k = 0; k < K; ++k) z = fmaf(w[k][i], win[k][i], z);
-                y[i] = silu_(z);
+                for (int k = 0; k < K - 1; ++k) window_slot(p.s0, q.n, k + 1, K, c, C, win[(j + 1 + k) % K]);
             }
-            store_row<T, VEC>(static_cast<T *>(p.y) + (long long)row * C, tile, lane, C, y);
-            if (p.sT && map.end[warp * S + s] >= 0) {
-                float *o = p.sT + (long long)map.end[warp * S + s] * C * K;
+        };
+        if (min(q.end, e) >= r + S) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = lane_channel<VEC>(tile, lane, i);
-                    if (c < C)
-#pragma unroll
-                        for (int k = 0; k < K; ++k) o[(long long)c * K + k] = win[k][i];
-                }
+            for (int s = 0; s < S; ++s) one(s, s);
+            if (q.end == r + S) close(r + S, S - 1);
+            rotate<K, W>(win, S % K);
+        } else {
+            const int n = min(S, e - r);
+#pragma unroll 1
+            for (int s = 0; s < n; ++s) {
+                one(s, 0);
+                if (q.end == r + s + 1) close(r + s + 1, 0);
+                rotate<K, W>(win, 1 % K);
             }
-#pragma unroll
-            for (int k = 0; k + 1 < K; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) win[k][i] = win[k + 1][i];
         }
+        y += (long long)S * C;
+        next = slot;
+        slot = slot + 1 == ST ? 0 : slot + 1;
     }
 }
 
 // ---------------------------------------------------------------- backward
 // dz = dy s (1 + z (1 - s)), s = sigmoid(z);  din[r] = sum_i w[i] dz[r+K-1-i] over the
-// sequence's rows;  dw[i] = sum_t dz[t] in[t-K+1+i]. A warp walks its S rows and the K - 1
-// behind them (whose dz reaches back into its own), holding the K gradients that are not
-// complete yet; input r is complete at row r+K-1 or where its sequence ends. Sums over rows
-// go to one slice of dw per CTA and are joined by a second kernel in a fixed order.
-template <typename T, bool VEC, int K>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p) {
-    constexpr int S = kConvRows, L = kConvWarps * S;
-    __shared__ RowMap<L> map;
-    __shared__ float red[kConvWarps][kTileChannels];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tiles = (p.C + kTileChannels - 1) / kTileChannels, block = blockIdx.x / tiles;
-    const int tile = blockIdx.x - block * tiles, row0 = block * L, wrow = row0 + warp * S, R = p.span.R, C = p.C;
-    const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
-
-    float w[K][4], dw[K][4];
-    load_weights<VEC, K>(p.w, tile, lane, C, w);
+// sequence's rows;  dw[i] = sum_t dz[t] in[t-K+1+i]. A walker goes on for the K - 1 rows
+// behind its piece, whose dz reaches back into it, and holds the K gradients that are not
+// complete yet: input r is complete at row r+K-1 or where its sequence ends. A walker's
+// sums for dw leave as one slice, and a second kernel joins the slices in a fixed order.
+template <typename T, bool AL, int K>
+__global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p) {
+    using RN = BwdRing<T, AL>;
+    constexpr int W = RN::W, S = kStageRows, ST = 4, TC = walk_channels<T>();
+    extern __shared__ __align__(16) char dyn[];
+    const int lane = threadIdx.x, C = p.C, R = p.span.R, units = (C + TC - 1) / TC;
+    const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
+    const int b = min(piece * p.piece, R), e = piece + 1 == p.pieces ? R : min(b + p.piece, R);
+    const int stop = b < e ? min(e + K - 1, R) : e;  // rows that are walked
+    const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R), walk_tensor<T>(p.dy, p.dy_stride, c0, C, R)},
+                  min(TC, C - c0) * (int)sizeof(T), lane};
+    auto load = [&](int at, int row) {
+        ring.load(at, 0, row, b, stop);
+        ring.load(at, 1, row, b, stop);
+    };
+#pragma unroll 1
+    for (int k = 0; k < ST - 1; ++k) {
+        if (b + k * S < stop) load(k, b + k * S);
+        cp_async_commit();
+    }
+    float w[K][W], dw[K][W];
+    load_weights<K, W>(p.w, c, C, w);
 #pragma unroll
-    for (int k = 0; k < K; ++k) dw[k][0] = dw[k][1] = dw[k][2] = dw[k][3] = 0.f;
+    for (int k = 0; k < K; ++k) vset(dw[k], 0.f);
     // an empty sequence's final window is its initial one
-    fill_rows<L>(map, p.span, row0, [&](int n) {
-        if (!p.ds0) return;
-        const long long c0 = ((long long)n * C + tile * kTileChannels) * K, c1 = ((long long)n * C + min(C, (tile + 1) * kTileChannels)) * K;
-        for (long long c = c0; c < c1; ++c) p.ds0[c] = p.dsT ? p.dsT[c] : 0.f;
-    });
-    if (wrow < R) {
-        int seq, start;
-        sequence_at<L>(map, row0, warp * S, lane, seq, start);
-        float win[K][4], acc[K][4];  // acc[j]: the gradient of input t-K+1+j, so far
-        load_window<T, VEC, K>(x, p.x_stride, p.s0, wrow, seq, start, tile, lane, C, win);
+    hand_through<W>(p.span, piece, p.pieces, lane, c, C, K, p.ds0, p.dsT);
+    if (b < e) {
+        Seq q = seq_of(p.span, b, lane);
+        // at the s-th row t of a stage win[(s + k) % K] is input t-K+1+k, acc[(s + k) % K] its gradient so far
+        float win[K][W], acc[K][W];
+        load_window<T, K, W>(static_cast<const T *>(p.x), p.x_stride, p.s0, b, q, c, C, win);
 #pragma unroll
-        for (int k = 0; k < K; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
-        int end = p.span.cu ? min(max(p.span.cu[seq + 1], 0), R) : min((seq + 1) * p.span.T, R);
-        // input r of the sequence (r < start: its window) is complete with gradient v
-        auto finish = [&](int r, float (&v)[4]) {
-            if (r >= wrow + S) return;
-            if (r >= start ? r < wrow : (start < wrow || !p.ds0 || r < start - K)) return;
-            const int slot = r - end + K;  // place in the final window
-            if (p.dsT && slot >= 0) {
-                float f[4];
-                window_slot<VEC>(p.dsT, seq, slot, K, tile, lane, C, f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += f[i];
+        for (int k = 0; k < K; ++k) vset(acc[k], 0.f);
+        T *dx = static_cast<T *>(p.dx);
+        // input r of the sequence (r < start: of its window) is complete with gradient v
+        auto finish = [&](int r, float (&v)[W]) {
+            if (r >= e) return;
+            if (r >= q.start ? r < b : (q.start < b || !p.ds0)) return;
+            const int place = r - q.end + K;  // in the final window
+            if (p.dsT && place >= 0) {
+                float f[W];
+                window_slot(p.dsT, q.n, place, K, c, C, f);
+                vadd(v, f, v);
             }
-            if (r >= start) {
-                store_row<T, VEC>(static_cast<T *>(p.dx) + (long long)r * C, tile, lane, C, v);
+            if (r >= q.start) {
+                put_row<AL>(dx + (long long)r * C, c, C, lane, v);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = lane_channel<VEC>(tile, lane, i);
-                    if (c < C) p.ds0[((long long)seq * C + c) * K + (r - start + K)] = v[i];
-                }
+                for (int i = 0; i < W; ++i)
+                    if (c + i < C) p.ds0[((long long)q.n * C + c + i) * K + (r - q.start + K)] = v[i];
             }
         };
-        // the oldest value of the first window of a sequence that starts here is no input of any row
+        // the oldest value of the window of a sequence that starts here is no input of any row
         auto oldest = [&]() {
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            finish(start - K, v);
+            float v[W];
+            vset(v, 0.f);
+            finish(q.start - K, v);
         };
-        if (start == wrow) oldest();
-        int t = wrow;
-        const int stop = min(wrow + S + K - 1, R);
+        if (q.start == b) oldest();
+        int slot = 0, next = ST - 1;
+        // one more turn than there are rows where the data ends there, for what the last sequence holds
+        const int turns = stop == R ? stop + 1 : stop;
 #pragma unroll 1
-        for (; t < stop; ++t) {
-            if (t == end) {
-                // the sequence is over: what it still holds is complete
+        for (int r = b; r < turns; r += S) {
+            cp_async_wait_group<ST - 2>();
+            __syncwarp();
+            const int ahead = r + (ST - 1) * S;
+            if (ahead < stop) load(next, ahead);
+            cp_async_commit();
+            // row r + s, with the oldest input in slot j; its gradient is complete after it
+            auto one = [&](int s, int j, bool own) {
+                float dz[W], z[W];
+                ring.get(slot, 0, s, r + s, win[(j + K - 1) % K]);
+                ring.get(slot, 1, s, r + s, dz);
+                vmul(w[0], win[j % K], z);
 #pragma unroll
-                for (int k = 0; k < K - 1; ++k) finish(t - K + 1 + k, acc[k]);
-                if (t >= wrow + S) break;
-                seq = map.start[t - row0];
-                if (seq < 0) break;  // offsets that do not cover the rows
-                start = t;
-                end = p.span.cu ? min(max(p.span.cu[seq + 1], 0), R) : min((seq + 1) * p.span.T, R);
-                oldest();
+                for (int k = 1; k < K; ++k) vfma(w[k], win[(j + k) % K], z, z);
 #pragma unroll
-                for (int k = 0; k < K; ++k) acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+                for (int i = 0; i < W; ++i) {
+                    const float sg = sig<T>(z[i]);
+                    dz[i] *= sg * fmaf(z[i], 1.f - sg, 1.f);
+                }
+                vmul(w[K - 1], dz, acc[(j + K - 1) % K]);  // the newest input's gradient begins here
 #pragma unroll
-                for (int k = 0; k < K - 1; ++k) window_slot<VEC>(p.s0, seq, k + 1, K, tile, lane, C, win[k]);
-            }
-            const Raw4<T> xr = load_row<T, VEC>(x + (long long)t * p.x_stride, tile, lane, C, true);
-            const Raw4<T> dr = load_row<T, VEC>(dy + (long long)t * p.dy_stride, tile, lane, C, true);
-            const bool own = t < wrow + S;
+                for (int k = 0; k + 1 < K; ++k) vfma(w[k], dz, acc[(j + k) % K], acc[(j + k) % K]);
+                if (own) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                win[K - 1][i] = raw_get(xr, i);
-                float z = 0.f;
+                    for (int k = 0; k < K; ++k) vfma(dz, win[(j + k) % K], dw[k], dw[k]);
+                }
+            };
+            // plain stages: all rows the piece's and of one sequence, whose windows are out of reach
+            const bool first = q.start >= b && q.start > r - K;
+            if (r + S <= e && q.end > r + S && !(first && p.ds0)) {
+                const int from = max(b, q.start);
 #pragma unroll
-                for (int k = 0; k < K; ++k) z = fmaf(w[k][i], win[k][i], z);
-                const float sg = 1.f / (1.f + expf(-z));
-                const float dz = raw_get(dr, i) * sg * fmaf(z, 1.f - sg, 1.f);
+                for (int s = 0; s < S; ++s) {
+                    one(s, s, true);
+                    const int row = r + s - (K - 1);
+                    if (s >= K - 1 || row >= from) put_row<AL>(dx + (long long)row * C, c, C, lane, acc[s % K]);
+                }
+                rotate<K, W>(win, S % K);
+                rotate<K, W>(acc, S % K);
+            } else {
+#pragma unroll 1
+                for (int s = 0; s < S; ++s) {
+                    const int t = r + s;
+                    if (t >= turns) break;
+                    if (t == q.end) {
+                        // the sequence is over: what it still holds is complete
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    acc[k][i] = fmaf(w[k][i], dz, acc[k][i]);
-                    if (own) dw[k][i] = fmaf(dz, win[k][i], dw[k][i]);
+                        for (int k = 0; k < K - 1; ++k) finish(t - K + 1 + k, acc[k]);
+                        if (t >= e) { r = turns; break; }
+                        q = seq_of(p.span, t, lane);
+                        oldest();
+#pragma unroll
+                        for (int k = 0; k < K; ++k) vset(acc[k], 0.f);
+#pragma unroll
+                        for (int k = 0; k < K - 1; ++k) window_slot(p.s0, q.n, k + 1, K, c, C, win[k]);
+                    }
+                    if (t >= stop) break;
+                    one(s, 0, t < e);
+                    finish(t - K + 1, acc[0]);
+                    rotate<K, W>(win, 1 % K);
+                    rotate<K, W>(acc, 1 % K);
                 }
             }
-            finish(t - K + 1, acc[0]);
-#pragma unroll
-            for (int k = 0; k + 1 < K; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) { acc[k][i] = acc[k + 1][i]; win[k][i] = win[k + 1][i]; }
-            acc[K - 1][0] = acc[K - 1][1] = acc[K - 1][2] = acc[K - 1][3] = 0.f;
+            next = slot;
+            slot = slot + 1 == ST ? 0 : slot + 1;
         }
-        // the last row of all: nothing follows
-        if (t == R && t == end && t < wrow + S + K - 1)
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k) finish(t - K + 1 + k, acc[k]);
     }
     if (!p.partial) return;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        __syncthreads();
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) red[warp][lane_channel<VEC>(0, lane, i)] = dw[k][i];
-        __syncthreads();
-        const int c = threadIdx.x;
-        if (c < kTileChannels && tile * kTileChannels + c < C) {
-            float s = 0.f;
-#pragma unroll
-            for (int j = 0; j < kConvWarps; ++j) s += red[j][c];
-            p.partial[((long long)block * K + k) * C + tile * kTileChannels + c] = s;
-        }
-    }
+        for (int i = 0; i < W; ++i)
+            if (c + i < C) p.partial[((long long)piece * K + k) * C + c + i] = dw[k][i];
 }
 
 // dw[c, k]: the sum of its slices. One warp column of 32 channels, the slices shared out
@@ -321,77 +345,98 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 #pragma unroll
         for (int k = 0; k < K; ++k) s[k] = win[k];
     }
-    static_cast<T *>(p.y)[i] = from_f32<T>(silu_(z));
+    static_cast<T *>(p.y)[i] = from_f32<T>(z * sig<T>(z));
 }
 
 // ---------------------------------------------------------------- host
-bool vec_ok(const void *p, long long stride, size_t esz) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % (4 * esz) == 0 && stride % 4 == 0);
+int units_of(int C, bool bf16) {
+    const int tc = bf16 ? walk_channels<__nv_bfloat16>() : walk_channels<float>();
+    return (C + tc - 1) / tc;
 }
 
-// Blocks of rows, and CTAs: one for each block and channel tile.
-long long conv_blocks(int rows) {
-    const int L = kConvWarps * kConvRows;
-    return rows > L ? (rows + L - 1) / L : 1;
+// Rows of a piece: stages for one wave of walkers (a few waves where the channels alone
+// make more).
+int piece_rows(int rows, int C, bool bf16) {
+    const int units = units_of(C, bf16), want = kConvSlots > units ? kConvSlots / units : 1;
+    const int each = rows / want > kMinPiece ? (int)(((long long)rows + want - 1) / want) : kMinPiece;
+    return (each + kStageRows - 1) / kStageRows * kStageRows;
 }
-long long conv_ctas(int rows, int C) { return conv_blocks(rows) * ((C + kTileChannels - 1) / kTileChannels); }
+int pieces_of(int rows, int piece) { return rows > piece ? (int)(((long long)rows + piece - 1) / piece) : 1; }
 
-template <typename T, bool VEC, int K> cudaError_t run_fwd(const ConvParams &p, cudaStream_t st) {
+template <typename T, typename P> cudaError_t run_walk(void (*kernel)(P), const P &p, int ring_bytes, cudaStream_t st) {
+    const long long grid = (long long)p.pieces * units_of(p.C, sizeof(T) == 2);
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     count_launch();
-    conv_fwd_kernel<T, VEC, K><<<(unsigned)conv_ctas(p.span.R, p.C), kConvThreads, 0, st>>>(p);
+    kernel<<<(unsigned)grid, 32, ring_bytes, st>>>(p);
     return cudaGetLastError();
 }
-template <typename T, bool VEC, int K> cudaError_t run_bwd(const ConvBwdParams &p, cudaStream_t st) {
-    count_launch();
-    conv_bwd_kernel<T, VEC, K><<<(unsigned)conv_ctas(p.span.R, p.C), kConvThreads, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+
+template <typename T, bool AL, int K> cudaError_t run_fwd(const ConvParams &p, cudaStream_t st) {
+    return run_walk<T>(conv_fwd_kernel<T, AL, K>, p, FwdRing<T, AL>::BYTES, st);
+}
+template <typename T, bool AL, int K> cudaError_t run_bwd(const ConvBwdParams &p, cudaStream_t st) {
+    const cudaError_t e = run_walk<T>(conv_bwd_kernel<T, AL, K>, p, BwdRing<T, AL>::BYTES, st);
     if (e != cudaSuccess || !p.dw) return e;
     count_launch();
-    conv_dw_kernel<<<dim3((p.C + 31) / 32, K), 256, 0, st>>>(p.partial, p.dw, (int)conv_blocks(p.span.R), p.C, K);
+    conv_dw_kernel<<<dim3((p.C + 31) / 32, K), 256, 0, st>>>(p.partial, p.dw, p.pieces, p.C, K);
     return cudaGetLastError();
 }
-template <typename T, bool VEC, int K> cudaError_t run_step(const ConvStepParams &p, cudaStream_t st) {
+template <typename T, int K> cudaError_t run_step(const ConvStepParams &p, cudaStream_t st) {
     const long long n = (long long)p.N * p.C;
     count_launch();
     conv_step_kernel<T, K><<<(unsigned)((n + 127) / 128), 128, 0, st>>>(p);
     return cudaGetLastError();
 }
 
-// Runs F<T, VEC, K> for the type, layout and window of a call.
-#define KDA_CONV_K(F, T, V, p, st)                                                                     \
-    switch (p.K) {                                                                                     \
-    case 1: return F<T, V, 1>(p, st); case 2: return F<T, V, 2>(p, st); case 3: return F<T, V, 3>(p, st); \
-    case 4: return F<T, V, 4>(p, st); case 5: return F<T, V, 5>(p, st); case 6: return F<T, V, 6>(p, st); \
-    case 7: return F<T, V, 7>(p, st); case 8: return F<T, V, 8>(p, st);                                \
-    }                                                                                                  \
+// Runs F<..., K> for the window of a call.
+#define KDA_CONV_K(K_, ...)                                       \
+    switch (K_) {                                                 \
+    case 1: return __VA_ARGS__ 1>(p, st);                         \
+    case 2: return __VA_ARGS__ 2>(p, st);                         \
+    case 3: return __VA_ARGS__ 3>(p, st);                         \
+    case 4: return __VA_ARGS__ 4>(p, st);                         \
+    case 5: return __VA_ARGS__ 5>(p, st);                         \
+    case 6: return __VA_ARGS__ 6>(p, st);                         \
+    case 7: return __VA_ARGS__ 7>(p, st);                         \
+    case 8: return __VA_ARGS__ 8>(p, st);                         \
+    }                                                             \
     return cudaErrorInvalidValue;
-#define KDA_CONV_PICK(F, p, bf16, vec, st)                                                             \
-    if (bf16) { if (vec) { KDA_CONV_K(F, __nv_bfloat16, true, p, st) } else { KDA_CONV_K(F, __nv_bfloat16, false, p, st) } } \
-    if (vec) { KDA_CONV_K(F, float, true, p, st) } else { KDA_CONV_K(F, float, false, p, st) }
+#define KDA_CONV_PICK(F, bf16, al)                                          \
+    if (bf16 && al) { KDA_CONV_K(p.K, F<__nv_bfloat16, true, ) }            \
+    if (bf16) { KDA_CONV_K(p.K, F<__nv_bfloat16, false, ) }                 \
+    if (al) { KDA_CONV_K(p.K, F<float, true, ) }                            \
+    KDA_CONV_K(p.K, F<float, false, )
 
 }  // namespace
 
-size_t conv_bwd_workspace_bytes(int rows, int C, int K) {
-    return sizeof(float) * (size_t)conv_blocks(rows) * C * K;
+size_t conv_bwd_workspace_bytes(int rows, int C, int K, bool bf16) {
+    return sizeof(float) * (size_t)pieces_of(rows, piece_rows(rows, C, bf16)) * C * K;
 }
 
-cudaError_t launch_conv(const ConvParams &p, bool bf16, cudaStream_t st) {
+cudaError_t launch_conv(ConvParams p, bool bf16, cudaStream_t st) {
     const size_t esz = bf16 ? 2 : 4;
-    const bool vec = p.C % 4 == 0 && vec_ok(p.x, p.x_stride, esz) && vec_ok(p.y, p.C, esz);
-    if (conv_ctas(p.span.R, p.C) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    KDA_CONV_PICK(run_fwd, p, bf16, vec, st)
+    p.piece = piece_rows(p.span.R, p.C, bf16);
+    p.pieces = pieces_of(p.span.R, p.piece);
+    Aligned al;
+    al.rows(p.x, p.x_stride, p.C, esz);
+    al.rows(p.y, p.C, p.C, esz);
+    KDA_CONV_PICK(run_fwd, bf16, al.ok)
 }
 
-cudaError_t launch_conv_bwd(const ConvBwdParams &p, bool bf16, cudaStream_t st) {
+cudaError_t launch_conv_bwd(ConvBwdParams p, bool bf16, cudaStream_t st) {
     const size_t esz = bf16 ? 2 : 4;
-    const bool vec = p.C % 4 == 0 && vec_ok(p.x, p.x_stride, esz) && vec_ok(p.dy, p.dy_stride, esz) && vec_ok(p.dx, p.C, esz);
-    if (conv_ctas(p.span.R, p.C) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    KDA_CONV_PICK(run_bwd, p, bf16, vec, st)
+    p.piece = piece_rows(p.span.R, p.C, bf16);
+    p.pieces = pieces_of(p.span.R, p.piece);
+    Aligned al;
+    al.rows(p.x, p.x_stride, p.C, esz);
+    al.rows(p.dy, p.dy_stride, p.C, esz);
+    al.rows(p.dx, p.C, p.C, esz);
+    KDA_CONV_PICK(run_bwd, bf16, al.ok)
 }
 
 cudaError_t launch_conv_step(const ConvStepParams &p, bool bf16, cudaStream_t st) {
-    if (bf16) { KDA_CONV_K(run_step, __nv_bfloat16, true, p, st) }
-    KDA_CONV_K(run_step, float, true, p, st)
+    if (bf16) { KDA_CONV_K(p.K, run_step<__nv_bfloat16, ) }
+    KDA_CONV_K(p.K, run_step<float, )
 }
 
 }  // namespace kda

@@ -2,7 +2,7 @@
 // causal convolution and gated scan (device pointers, strides in elements).
 #pragma once
 
-#include "kda_rows.cuh"
+#include "kda_walk.cuh"
 
 namespace kda {
 
@@ -40,6 +40,7 @@ struct ConvParams {
     const float *s0;     // [N, C, K] windows or null
     float *sT;
     void *y;
+    int piece, pieces;   // rows of a walker, walkers of a channel unit
 };
 
 struct ConvBwdParams {
@@ -51,7 +52,8 @@ struct ConvBwdParams {
     const float *s0, *dsT;
     void *dx;
     float *dw, *ds0;
-    float *partial;      // [slices, K, C]
+    float *partial;      // [pieces, K, C]
+    int piece, pieces;
 };
 
 struct ConvStepParams {
@@ -63,15 +65,15 @@ struct ConvStepParams {
     int N, C, K;
 };
 
-// Scratch of a scan whose rows are cut into chunks.
-struct ScanChain {
-    int *status;         // 1: a wait gave up
-    unsigned *ticket;
-    unsigned *flags;     // [chunks, tiles]
-    float2 *agg;         // [chunks, tiles, kTileChannels]: a chunk as the map c -> A c + H
-    float *inc;          // [chunks / group, tiles, kTileChannels]: the state behind a group
-    int chunks, tiles, group;
-    int stall;           // test of the bounded waits
+// How a scan's rows are cut into pieces, one after another:
+//   kCutBatch  `per` pieces of `rows` rows in each sequence of T rows (the last shorter)
+//   kCutSeqs   a piece per sequence of cu
+//   kCutRows   pieces of `rows` rows, wherever sequences begin
+enum : int { kCutBatch = 0, kCutSeqs = 1, kCutRows = 2 };
+struct ScanCut {
+    int kind, pieces, per, rows;
+    int carries;         // whether a piece may continue a sequence of the one before
+    float2 *maps;        // [pieces, D]: a piece as the map c -> A c + H (A < 0: of no c)
 };
 
 struct ScanParams {
@@ -82,9 +84,8 @@ struct ScanParams {
     const float *s0;     // [N, D] or null
     float *sT;
     void *h;
-    int has_lb;
-    float lb;
-    ScanChain chain;
+    float lb;            // -inf without a bound
+    ScanCut cut;
 };
 
 struct ScanBwdParams {
@@ -95,9 +96,8 @@ struct ScanBwdParams {
     const float *s0, *dsT;
     void *dx, *dg;
     float *ds0;
-    int has_lb;
-    float lb;
-    ScanChain chain;
+    float lb;            // -inf without a bound
+    ScanCut cut;
 };
 
 struct ScanStepParams {
@@ -107,22 +107,21 @@ struct ScanStepParams {
     float *state_out;
     void *h;
     int N, D;
-    int has_lb;
-    float lb;
+    float lb;            // -inf without a bound
 };
 
 cudaError_t launch_rms_norm(const NormParams &p, bool bf16, cudaStream_t st);
 size_t rms_norm_bwd_workspace_bytes(long long rows, int D, bool bf16, bool weight);
 cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, bool bf16, cudaStream_t st);
 
-cudaError_t launch_conv(const ConvParams &p, bool bf16, cudaStream_t st);
-size_t conv_bwd_workspace_bytes(int rows, int C, int K);
-cudaError_t launch_conv_bwd(const ConvBwdParams &p, bool bf16, cudaStream_t st);
+cudaError_t launch_conv(ConvParams p, bool bf16, cudaStream_t st);
+size_t conv_bwd_workspace_bytes(int rows, int C, int K, bool bf16);
+cudaError_t launch_conv_bwd(ConvBwdParams p, bool bf16, cudaStream_t st);
 cudaError_t launch_conv_step(const ConvStepParams &p, bool bf16, cudaStream_t st);
 
-size_t scan_workspace_bytes(int rows, int D, bool bf16, bool backward);
-cudaError_t launch_scan(ScanParams p, bool bf16, bool sigmoid, void *workspace, cudaStream_t st);
-cudaError_t launch_scan_bwd(ScanBwdParams p, bool bf16, bool sigmoid, void *workspace, cudaStream_t st);
+size_t scan_workspace_bytes(const RowSpan &span, const int32_t *cu_host, int D, bool bf16);
+cudaError_t launch_scan(ScanParams p, const int32_t *cu_host, bool bf16, bool sigmoid, void *workspace, cudaStream_t st);
+cudaError_t launch_scan_bwd(ScanBwdParams p, const int32_t *cu_host, bool bf16, bool sigmoid, void *workspace, cudaStream_t st);
 cudaError_t launch_scan_step(const ScanStepParams &p, bool bf16, bool sigmoid, cudaStream_t st);
 
 }  // namespace kda

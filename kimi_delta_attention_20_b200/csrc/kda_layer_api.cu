@@ -1,15 +1,14 @@
 // Entry points of the operators around the state update (RMS norm, causal convolution,
-// gated scan): argument validation and launch. No allocation, no synchronisation but in
-// the status queries.
+// gated scan): argument validation and launch. No allocation, no synchronisation.
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/kda.h"
 #include "kda_layer.cuh"
 
 namespace kda {
-void record_cuda_error(int e);                                      // kda_api.cu
-kda_status read_status_word(const void *word, cudaStream_t st);    // kda_api.cu
-bool token_conv_supported(int K);                                   // kda_token.cu
+void record_cuda_error(int e);      // kda_api.cu
+bool token_conv_supported(int K);   // kda_token.cu
 }  // namespace kda
 
 namespace {
@@ -123,22 +122,13 @@ template <typename Args> kda_status scan_shape(const Args *a, kda::RowSpan *span
     return check_span(a->B, a->T, a->N, a->cu_seqlens, a->cu_seqlens_host, span);
 }
 
-template <typename Args> kda_status scan_workspace(const Args *a, bool backward, size_t *bytes) {
+template <typename Args> kda_status scan_workspace(const Args *a, size_t *bytes) {
     if (!a || !bytes) return KDA_ERR_INVALID_ARGUMENT;
     kda::RowSpan span;
     kda_status s = scan_shape(a, &span);
     if (s != KDA_OK) return s;
-    *bytes = kda::scan_workspace_bytes(span.R, a->D, a->dtype == KDA_DTYPE_BF16, backward);
+    *bytes = kda::scan_workspace_bytes(span, a->cu_seqlens_host, a->D, a->dtype == KDA_DTYPE_BF16);
     return KDA_OK;
-}
-
-template <typename Args> kda_status scan_status(const Args *a, bool backward, void *stream) {
-    size_t need = 0;
-    kda_status s = scan_workspace(a, backward, &need);
-    if (s != KDA_OK) return s;
-    if (need == 0) return KDA_OK;  // one chunk: nothing waits
-    if (!a->workspace) return KDA_ERR_WORKSPACE;
-    return kda::read_status_word(a->workspace, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -268,7 +258,7 @@ kda_status kda_causal_conv_bwd_workspace_size(const kda_conv_bwd_args *a, size_t
     kda_status s = check_conv_shape(a->dtype, a->C, a->K);
     if (s == KDA_OK) s = check_span(a->B, a->T, a->N, a->cu_seqlens, a->cu_seqlens_host, &span);
     if (s != KDA_OK) return s;
-    *bytes = a->dconv_w ? kda::conv_bwd_workspace_bytes(span.R, a->C, a->K) : 0;
+    *bytes = a->dconv_w ? kda::conv_bwd_workspace_bytes(span.R, a->C, a->K, a->dtype == KDA_DTYPE_BF16) : 0;
     return KDA_OK;
 }
 
@@ -300,11 +290,11 @@ kda_status kda_causal_conv_bwd(const kda_conv_bwd_args *a, void *stream) {
     return launched(kda::launch_conv_bwd(p, a->dtype == KDA_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
 }
 
-kda_status kda_gated_scan_workspace_size(const kda_scan_args *a, size_t *bytes) { return scan_workspace(a, false, bytes); }
+kda_status kda_gated_scan_workspace_size(const kda_scan_args *a, size_t *bytes) { return scan_workspace(a, bytes); }
 
 kda_status kda_gated_scan(const kda_scan_args *a, void *stream) {
     size_t need = 0;
-    kda_status s = scan_workspace(a, false, &need);
+    kda_status s = scan_workspace(a, &need);
     if (s != KDA_OK) return s;
     kda::ScanParams p{};
     check_span(a->B, a->T, a->N, a->cu_seqlens, nullptr, &p.span);
@@ -317,17 +307,13 @@ kda_status kda_gated_scan(const kda_scan_args *a, void *stream) {
     c.output(a->h, any, p.span.R, a->D, esz);
     c.output(a->final_state, false, p.span.N, a->D, 4);
     if (c.bad || !c.apart()) return KDA_ERR_INVALID_ARGUMENT;
-    if (!workspace_ok(a->workspace, a->workspace_bytes, need, 256)) return KDA_ERR_WORKSPACE;
+    if (!workspace_ok(a->workspace, a->workspace_bytes, need, 16)) return KDA_ERR_WORKSPACE;
     if (!any && !a->final_state) return KDA_OK;
     p.x = a->x; p.g = a->g; p.D = a->D; p.s0 = a->initial_state; p.sT = a->final_state; p.h = a->h;
-    p.has_lb = a->has_lower_bound ? 1 : 0;
-    p.lb = a->lower_bound;
-    p.chain.stall = a->debug_flags & KDA_DEBUG_STALL_FIRST_WAIT ? 1 : 0;
-    return launched(kda::launch_scan(p, a->dtype == KDA_DTYPE_BF16, a->gate == KDA_SCAN_GATE_SIGMOID, a->workspace,
+    p.lb = a->has_lower_bound ? a->lower_bound : -INFINITY;
+    return launched(kda::launch_scan(p, a->cu_seqlens_host, a->dtype == KDA_DTYPE_BF16, a->gate == KDA_SCAN_GATE_SIGMOID, a->workspace,
                                      static_cast<cudaStream_t>(stream)));
 }
-
-kda_status kda_gated_scan_status(const kda_scan_args *a, void *stream) { return scan_status(a, false, stream); }
 
 kda_status kda_gated_scan_step(const kda_scan_step_args *a, void *stream) {
     if (!a || !dtype_ok(a->dtype) || a->N < 0 || a->D < 1) return KDA_ERR_INVALID_ARGUMENT;
@@ -347,17 +333,16 @@ kda_status kda_gated_scan_step(const kda_scan_step_args *a, void *stream) {
     if (c.bad || !a->state || !c.apart()) return KDA_ERR_INVALID_ARGUMENT;
     p.x = a->x; p.g = a->g; p.state = a->state; p.state_out = to; p.h = a->h;
     p.N = a->N; p.D = a->D;
-    p.has_lb = a->has_lower_bound ? 1 : 0;
-    p.lb = a->lower_bound;
+    p.lb = a->has_lower_bound ? a->lower_bound : -INFINITY;
     return launched(kda::launch_scan_step(p, a->dtype == KDA_DTYPE_BF16, a->gate == KDA_SCAN_GATE_SIGMOID,
                                           static_cast<cudaStream_t>(stream)));
 }
 
-kda_status kda_gated_scan_bwd_workspace_size(const kda_scan_bwd_args *a, size_t *bytes) { return scan_workspace(a, true, bytes); }
+kda_status kda_gated_scan_bwd_workspace_size(const kda_scan_bwd_args *a, size_t *bytes) { return scan_workspace(a, bytes); }
 
 kda_status kda_gated_scan_bwd(const kda_scan_bwd_args *a, void *stream) {
     size_t need = 0;
-    kda_status s = scan_workspace(a, true, &need);
+    kda_status s = scan_workspace(a, &need);
     if (s != KDA_OK) return s;
     kda::ScanBwdParams p{};
     check_span(a->B, a->T, a->N, a->cu_seqlens, nullptr, &p.span);
@@ -374,17 +359,13 @@ kda_status kda_gated_scan_bwd(const kda_scan_bwd_args *a, void *stream) {
     c.output(a->dg, any, p.span.R, a->D, esz);
     c.output(a->dinitial_state, false, p.span.N, a->D, 4);
     if (c.bad || !c.apart()) return KDA_ERR_INVALID_ARGUMENT;
-    if (!workspace_ok(a->workspace, a->workspace_bytes, need, 256)) return KDA_ERR_WORKSPACE;
+    if (!workspace_ok(a->workspace, a->workspace_bytes, need, 16)) return KDA_ERR_WORKSPACE;
     if (!any && !a->dinitial_state) return KDA_OK;
     p.x = a->x; p.g = a->g; p.h = a->h; p.dout = a->dout; p.D = a->D;
     p.s0 = a->initial_state; p.dsT = a->dfinal_state;
     p.dx = a->dx; p.dg = a->dg; p.ds0 = a->dinitial_state;
-    p.has_lb = a->has_lower_bound ? 1 : 0;
-    p.lb = a->lower_bound;
-    p.chain.stall = a->debug_flags & KDA_DEBUG_STALL_FIRST_WAIT ? 1 : 0;
-    return launched(kda::launch_scan_bwd(p, a->dtype == KDA_DTYPE_BF16, sig, a->workspace, static_cast<cudaStream_t>(stream)));
+    p.lb = a->has_lower_bound ? a->lower_bound : -INFINITY;
+    return launched(kda::launch_scan_bwd(p, a->cu_seqlens_host, a->dtype == KDA_DTYPE_BF16, sig, a->workspace, static_cast<cudaStream_t>(stream)));
 }
-
-kda_status kda_gated_scan_bwd_status(const kda_scan_bwd_args *a, void *stream) { return scan_status(a, true, stream); }
 
 }  // extern "C"

@@ -1,7 +1,5 @@
 """Gated linear recurrence over packed sequences, its single token and its gradients
 against the 64-bit form."""
-import ctypes
-
 import pytest
 import torch
 
@@ -179,28 +177,3 @@ def test_scan_autograd():
         for n, a, b in (("x", x, X), ("g", g, G), ("s0", s0, S)):
             # runs of at most 100 steps, each off by some 20 u of what it carries
             within(n, a.grad, b.grad, 100 * 30 * U * b.grad.abs().max())
-
-
-def test_scan_status_reports_a_wait_that_gave_up():
-    """With the first chunk's report withheld the waits on it run out, the kernel ends, and the
-    status says so; the next call is right again."""
-    from kimi_delta_attention_20_b200 import _abi
-    lib = _abi.load()
-    T, D = 300, 8
-    x, g = draw(1, T, D, dtype=torch.float32, seed=1), gates(T, D, False, torch.float32, 2)[None]
-    h = torch.empty_like(x)
-    st = torch.cuda.current_stream().cuda_stream
-    a = _abi.ScanArgs(_abi.KDA_DTYPE_F32, 0, 1, T, D, x.data_ptr(), 0, g.data_ptr(), 0, h.data_ptr())
-    a.N = 1
-    n = ctypes.c_size_t(0)
-    assert lib.kda_gated_scan_workspace_size(ctypes.byref(a), ctypes.byref(n)) == 0 and n.value
-    ws = torch.empty(n.value, dtype=torch.uint8, device=DEV)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), n.value
-    a.debug_flags = _abi.KDA_DEBUG_STALL_FIRST_WAIT
-    assert lib.kda_gated_scan(ctypes.byref(a), st) == 0
-    assert lib.kda_gated_scan_status(ctypes.byref(a), st) == _abi.KDA_ERR_TIMEOUT
-    a.debug_flags = 0
-    assert lib.kda_gated_scan(ctypes.byref(a), st) == 0
-    assert lib.kda_gated_scan_status(ctypes.byref(a), st) == 0
-    want, _, e, _ = ref.scan(x[0], g[0], [T])
-    within("h", h[0], want, want.abs() * U + e)
