@@ -372,6 +372,7 @@ KDA_API kda_status kda_chunk_fwd_noalloc_status(const kda_chunk_args *args, void
  * Root-mean-square norm of `rows` rows of D channels (1 <= D <= 16384), with the
  * options that a layer needs:
  *     s = x (+ residual),  y = s / sqrt(mean(s^2) + eps) * weight * sigmoid(gate)
+ * (a residual or a gate, not both).
  * The gate is the full-rank output gate of page "atlas_core/kimi_k3/kda.rs"
  * (`full_rank_output_gate`) for whole sequences. The norm is taken of the fp32 sum;
  * residual_out receives the sum in the activations' dtype.

@@ -7,19 +7,21 @@
 //
 // Bound by HBM: 4 bytes an element forward, 6 backward (bf16). A walker slides the window
 // down its piece of the rows in registers. Nothing is carried between pieces but K - 1
-// rows that are read twice, so pieces are cut for full waves of walkers: twelve an SM with
-// rings of 16 KiB, since the backward needs the arithmetic of many warps beside the bytes
-// in flight.
+// rows that are read twice, so pieces are cut for full waves of walkers: sixteen an SM with
+// rings of 12 KiB, since they need the arithmetic of many warps beside the bytes in flight
+// (9 walkers of 24 KiB: 53 us for 8192 x 6144, 12 of 16 KiB: 43, 16 of 12 KiB: 42).
 #include "kda_layer.cuh"
 
 namespace kda {
 
 namespace {
 
-constexpr int kConvSlots = 148 * 12;  // walkers that run at the same time
+constexpr int kConvSlots = 148 * 16;  // walkers that run at the same time
 constexpr int kMinPiece = 32;         // rows of a piece, at least
-template <typename T, bool AL> using FwdRing = Ring<T, AL, 1, 8>;
-template <typename T, bool AL> using BwdRing = Ring<T, AL, 2, 4>;
+constexpr int kLB = 8, kStage = 8;     // bytes of a lane, rows of a stage
+constexpr int kFwdStages = 6, kBwdStages = 3;
+template <typename T, int G> using FwdRing = Ring<T, G, kLB, kStage, 1, kFwdStages>;
+template <typename T, int G> using BwdRing = Ring<T, G, kLB, kStage, 2, kBwdStages>;
 
 // sigmoid, by the SFU where the result is rounded to bf16.
 template <typename T> __device__ __forceinline__ float sig(float z) {
@@ -70,13 +72,14 @@ template <int K, int W> __device__ __forceinline__ void rotate(float (&win)[K][W
 }
 
 // ---------------------------------------------------------------- forward
-template <typename T, bool AL, int K>
+template <typename T, int G, int K>
 __global__ void __launch_bounds__(32) conv_fwd_kernel(const __grid_constant__ ConvParams p) {
-    using RN = FwdRing<T, AL>;
-    constexpr int W = RN::W, S = kStageRows, ST = 8, TC = walk_channels<T>();
+    using RN = FwdRing<T, G>;
+    constexpr int W = RN::W, S = kStage, ST = kFwdStages, TC = walk_channels<T, kLB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, C = p.C, R = p.span.R, units = (C + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
+    const bool full = c0 + TC <= C;
     const int b = min(piece * p.piece, R), e = piece + 1 == p.pieces ? R : min(b + p.piece, R);
     const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R)}, min(TC, C - c0) * (int)sizeof(T), lane};
 #pragma unroll 1
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(32) conv_fwd_kernel(const __grid_constant__ Co
             for (int k = 1; k < K; ++k) vfma(w[k], win[(j + k) % K], z, z);
 #pragma unroll
             for (int i = 0; i < W; ++i) z[i] *= sig<T>(z[i]);
-            put_row<AL>(y + (long long)s * C, c, C, lane, z);
+            put_row<G>(y + (long long)s * C, c, C, lane, full, z);
         };
         // behind the last row of a sequence, its last K inputs in slots j, j + 1 ..
         auto close = [&](int row, int j) {
@@ -153,13 +156,14 @@ __global__ void __launch_bounds__(32) conv_fwd_kernel(const __grid_constant__ Co
 // behind its piece, whose dz reaches back into it, and holds the K gradients that are not
 // complete yet: input r is complete at row r+K-1 or where its sequence ends. A walker's
 // sums for dw leave as one slice, and a second kernel joins the slices in a fixed order.
-template <typename T, bool AL, int K>
+template <typename T, int G, int K>
 __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p) {
-    using RN = BwdRing<T, AL>;
-    constexpr int W = RN::W, S = kStageRows, ST = 4, TC = walk_channels<T>();
+    using RN = BwdRing<T, G>;
+    constexpr int W = RN::W, S = kStage, ST = kBwdStages, TC = walk_channels<T, kLB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, C = p.C, R = p.span.R, units = (C + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
+    const bool full = c0 + TC <= C;
     const int b = min(piece * p.piece, R), e = piece + 1 == p.pieces ? R : min(b + p.piece, R);
     const int stop = b < e ? min(e + K - 1, R) : e;  // rows that are walked
     const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R), walk_tensor<T>(p.dy, p.dy_stride, c0, C, R)},
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ Co
                 vadd(v, f, v);
             }
             if (r >= q.start) {
-                put_row<AL>(dx + (long long)r * C, c, C, lane, v);
+                put_row<G>(dx + (long long)r * C, c, C, lane, full, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < W; ++i)
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ Co
                 for (int s = 0; s < S; ++s) {
                     one(s, s, true);
                     const int row = r + s - (K - 1);
-                    if (s >= K - 1 || row >= from) put_row<AL>(dx + (long long)row * C, c, C, lane, acc[s % K]);
+                    if (s >= K - 1 || row >= from) put_row<G>(dx + (long long)row * C, c, C, lane, full, acc[s % K]);
                 }
                 rotate<K, W>(win, S % K);
                 rotate<K, W>(acc, S % K);
@@ -291,23 +295,11 @@ __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ Co
             if (c + i < C) p.partial[((long long)piece * K + k) * C + c + i] = dw[k][i];
 }
 
-// dw[c, k]: the sum of its slices. One warp column of 32 channels, the slices shared out
-// over the CTA's warps and joined in a fixed order.
-__global__ void __launch_bounds__(256) conv_dw_kernel(const float *partial, float *dw, int slices, int C, int K) {
-    __shared__ float red[8][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
-    float s = 0.f;
-    if (c < C)
-        for (int j = warp; j < slices; j += 8) s += partial[((long long)j * K + k) * C + c];
-    red[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < C) {
-        float v = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v += red[j][lane];
-        dw[(long long)c * K + k] = v;
-    }
+// dw[c, k]: the sum of its slices [K, C].
+__global__ void __launch_bounds__(1024) conv_dw_kernel(const float *partial, float *dw, int slices, int C, int K) {
+    const long long cols = (long long)K * C, col = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
+    const float v = slice_sum(partial, slices, cols, col);
+    if (threadIdx.x < 32 && col < cols) dw[col % C * K + col / C] = v;
 }
 
 // ---------------------------------------------------------------- single token
@@ -350,7 +342,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 
 // ---------------------------------------------------------------- host
 int units_of(int C, bool bf16) {
-    const int tc = bf16 ? walk_channels<__nv_bfloat16>() : walk_channels<float>();
+    const int tc = bf16 ? walk_channels<__nv_bfloat16, kLB>() : walk_channels<float, kLB>();
     return (C + tc - 1) / tc;
 }
 
@@ -359,7 +351,7 @@ int units_of(int C, bool bf16) {
 int piece_rows(int rows, int C, bool bf16) {
     const int units = units_of(C, bf16), want = kConvSlots > units ? kConvSlots / units : 1;
     const int each = rows / want > kMinPiece ? (int)(((long long)rows + want - 1) / want) : kMinPiece;
-    return (each + kStageRows - 1) / kStageRows * kStageRows;
+    return (each + kStage - 1) / kStage * kStage;
 }
 int pieces_of(int rows, int piece) { return rows > piece ? (int)(((long long)rows + piece - 1) / piece) : 1; }
 
@@ -371,14 +363,14 @@ template <typename T, typename P> cudaError_t run_walk(void (*kernel)(P), const 
     return cudaGetLastError();
 }
 
-template <typename T, bool AL, int K> cudaError_t run_fwd(const ConvParams &p, cudaStream_t st) {
-    return run_walk<T>(conv_fwd_kernel<T, AL, K>, p, FwdRing<T, AL>::BYTES, st);
+template <typename T, int G, int K> cudaError_t run_fwd(const ConvParams &p, cudaStream_t st) {
+    return run_walk<T>(conv_fwd_kernel<T, G, K>, p, FwdRing<T, G>::BYTES, st);
 }
-template <typename T, bool AL, int K> cudaError_t run_bwd(const ConvBwdParams &p, cudaStream_t st) {
-    const cudaError_t e = run_walk<T>(conv_bwd_kernel<T, AL, K>, p, BwdRing<T, AL>::BYTES, st);
+template <typename T, int G, int K> cudaError_t run_bwd(const ConvBwdParams &p, cudaStream_t st) {
+    const cudaError_t e = run_walk<T>(conv_bwd_kernel<T, G, K>, p, BwdRing<T, G>::BYTES, st);
     if (e != cudaSuccess || !p.dw) return e;
     count_launch();
-    conv_dw_kernel<<<dim3((p.C + 31) / 32, K), 256, 0, st>>>(p.partial, p.dw, p.pieces, p.C, K);
+    conv_dw_kernel<<<(unsigned)(((long long)p.C * K + 31) / 32), 1024, 0, st>>>(p.partial, p.dw, p.pieces, p.C, K);
     return cudaGetLastError();
 }
 template <typename T, int K> cudaError_t run_step(const ConvStepParams &p, cudaStream_t st) {
@@ -401,11 +393,14 @@ template <typename T, int K> cudaError_t run_step(const ConvStepParams &p, cudaS
     case 8: return __VA_ARGS__ 8>(p, st);                         \
     }                                                             \
     return cudaErrorInvalidValue;
-#define KDA_CONV_PICK(F, bf16, al)                                          \
-    if (bf16 && al) { KDA_CONV_K(p.K, F<__nv_bfloat16, true, ) }            \
-    if (bf16) { KDA_CONV_K(p.K, F<__nv_bfloat16, false, ) }                 \
-    if (al) { KDA_CONV_K(p.K, F<float, true, ) }                            \
-    KDA_CONV_K(p.K, F<float, false, )
+#define KDA_CONV_PICK(F, bf16, g)                                           \
+    if (bf16 && g == 16) { KDA_CONV_K(p.K, F<__nv_bfloat16, 16, ) }         \
+    if (bf16 && g == 8) { KDA_CONV_K(p.K, F<__nv_bfloat16, 8, ) }           \
+    if (bf16 && g == 4) { KDA_CONV_K(p.K, F<__nv_bfloat16, 4, ) }           \
+    if (bf16) { KDA_CONV_K(p.K, F<__nv_bfloat16, 2, ) }                     \
+    if (g == 16) { KDA_CONV_K(p.K, F<float, 16, ) }                         \
+    if (g == 8) { KDA_CONV_K(p.K, F<float, 8, ) }                           \
+    KDA_CONV_K(p.K, F<float, 4, )
 
 }  // namespace
 
@@ -417,21 +412,21 @@ cudaError_t launch_conv(ConvParams p, bool bf16, cudaStream_t st) {
     const size_t esz = bf16 ? 2 : 4;
     p.piece = piece_rows(p.span.R, p.C, bf16);
     p.pieces = pieces_of(p.span.R, p.piece);
-    Aligned al;
-    al.rows(p.x, p.x_stride, p.C, esz);
-    al.rows(p.y, p.C, p.C, esz);
-    KDA_CONV_PICK(run_fwd, bf16, al.ok)
+    RowAccess ac;
+    ac.rows(p.x, p.x_stride, p.C, esz);
+    ac.rows(p.y, p.C, p.C, esz);
+    KDA_CONV_PICK(run_fwd, bf16, ac.g())
 }
 
 cudaError_t launch_conv_bwd(ConvBwdParams p, bool bf16, cudaStream_t st) {
     const size_t esz = bf16 ? 2 : 4;
     p.piece = piece_rows(p.span.R, p.C, bf16);
     p.pieces = pieces_of(p.span.R, p.piece);
-    Aligned al;
-    al.rows(p.x, p.x_stride, p.C, esz);
-    al.rows(p.dy, p.dy_stride, p.C, esz);
-    al.rows(p.dx, p.C, p.C, esz);
-    KDA_CONV_PICK(run_bwd, bf16, al.ok)
+    RowAccess ac;
+    ac.rows(p.x, p.x_stride, p.C, esz);
+    ac.rows(p.dy, p.dy_stride, p.C, esz);
+    ac.rows(p.dx, p.C, p.C, esz);
+    KDA_CONV_PICK(run_bwd, bf16, ac.g())
 }
 
 cudaError_t launch_conv_step(const ConvStepParams &p, bool bf16, cudaStream_t st) {

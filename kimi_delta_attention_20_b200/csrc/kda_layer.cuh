@@ -72,8 +72,9 @@ struct ConvStepParams {
 enum : int { kCutBatch = 0, kCutSeqs = 1, kCutRows = 2 };
 struct ScanCut {
     int kind, pieces, per, rows;
+    int lb;              // bytes of a lane
     int carries;         // whether a piece may continue a sequence of the one before
-    float2 *maps;        // [pieces, D]: a piece as the map c -> A c + H (A < 0: of no c)
+    void *maps;          // [pieces, channels of whole units] pairs (A, H): a piece as the map c -> A c + H
 };
 
 struct ScanParams {
@@ -111,6 +112,7 @@ struct ScanStepParams {
 };
 
 cudaError_t launch_rms_norm(const NormParams &p, bool bf16, cudaStream_t st);
+cudaError_t launch_rms_norm_quant(const NormParams &p, bool bf16, int g, cudaStream_t st);
 size_t rms_norm_bwd_workspace_bytes(long long rows, int D, bool bf16, bool weight);
 cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, bool bf16, cudaStream_t st);
 

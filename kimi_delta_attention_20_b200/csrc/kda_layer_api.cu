@@ -140,6 +140,7 @@ kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
     kda_status s = check_norm_shape(a->dtype, a->weight_dtype, a->rows, a->D, a->eps);
     if (s != KDA_OK) return s;
     if (a->group_size != 0 && a->group_size != 32 && a->group_size != 64 && a->group_size != 128) return KDA_ERR_UNSUPPORTED;
+    if (a->residual && a->gate) return KDA_ERR_UNSUPPORTED;
     if (a->rows == 0) return KDA_OK;
     const size_t esz = size_of(a->dtype);
     kda::NormParams p{};
@@ -187,6 +188,7 @@ kda_status kda_rms_norm_bwd(const kda_rms_norm_bwd_args *a, void *stream) {
     size_t need = 0;
     kda_status s = kda_rms_norm_bwd_workspace_size(a, &need);
     if (s != KDA_OK) return s;
+    if (a->dresidual && a->gate) return KDA_ERR_UNSUPPORTED;
     const size_t esz = size_of(a->dtype), wsz = size_of(a->weight_dtype);
     kda::NormBwdParams p{};
     Checker c;

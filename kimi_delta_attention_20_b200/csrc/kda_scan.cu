@@ -25,11 +25,12 @@ namespace kda {
 
 namespace {
 
-// Walkers that run at the same time, with rings of about 32 KiB: 8 stages of two tensors,
-// 5 of three, 4 of four.
-constexpr int kWalkerSlots = 148 * 6;
-constexpr int ring_stages(int tensors) { return tensors == 2 ? 8 : tensors == 3 ? 5 : 4; }
-template <typename T, bool AL, int N> using ScanRing = Ring<T, AL, N, ring_stages(N)>;
+// Walkers that run at the same time, with rings of about 30 KiB.
+constexpr int kWalkerSlots = 148 * 7;
+constexpr int kMinPiece = 64;       // rows of a piece, at least
+constexpr int kStage = 8;  // rows of a stage
+constexpr int ring_stages(int lb, int tensors) { return 120 / lb / tensors; }
+template <typename T, int G, int LB, int N> using ScanRing = Ring<T, G, LB, kStage, N, ring_stages(LB, N)>;
 
 // a of the gate input, and the weight b of x in the sigmoid form: 1 - a without the
 // cancellation, since a is close to 1 where memories are long. lb is -inf without a bound.
@@ -86,25 +87,42 @@ __device__ __forceinline__ int piece_of(const ScanCut &cut, const RowSpan &sp, i
     return min(row / cut.rows, cut.pieces - 1);
 }
 
-// c <- the state behind pieces `first`, first + step, .. before `piece`. A piece where the
-// sequence begins leaves nothing of what came before, not even as 0 x inf.
+// A lane's channels of a piece's map: A and H of each, W pairs side by side. A map where a
+// sequence begins leaves nothing of what came before, not even as 0 x inf: its A is below 0.
+template <int W> struct __align__(W == 1 ? 8 : 16) Map {
+    float2 ch[W];
+};
+
+// The map of piece 0 of the lane whose first channel is c; a piece's maps take its channel
+// units in full.
+template <int W> __device__ __forceinline__ Map<W> *lane_map(const ScanCut &cut, int c) {
+    return static_cast<Map<W> *>(cut.maps) + c / W;
+}
+
+// c <- the state behind pieces first, first + step, .. before `piece`. at: the lane's map of
+// piece 0, `pitch` maps apart from the next piece's.
 template <int W>
-__device__ __forceinline__ void compose(const float2 *maps, int first, int piece, int step, int c0, int D, float (&c)[W]) {
-    constexpr int BATCH = 16 / W;
-#pragma unroll
-    for (int i = 0; i < W; ++i) c[i] = 0.f;
+__device__ __forceinline__ void compose(const Map<W> *at, long long pitch, int first, int piece, int step, float (&c)[W]) {
+    vset(c, 0.f);
+    constexpr int BATCH = 8;  // loads in flight
     for (int k = first; k != piece;) {
-        float2 m[BATCH][W];
+        Map<W> m[BATCH];
         const int n = min(BATCH, (piece - k) * step);
 #pragma unroll
         for (int u = 0; u < BATCH; ++u)
+            if (u < n) {
+                const float4 *q = reinterpret_cast<const float4 *>(at + (long long)(k + u * step) * pitch);
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                m[u][i] = u < n && c0 + i < D ? maps[(long long)(k + u * step) * D + c0 + i] : make_float2(1.f, 0.f);
+                for (int j = 0; j < (W + 1) / 2; ++j) {
+                    if constexpr (W == 1) m[u].ch[0] = *reinterpret_cast<const float2 *>(q);
+                    else reinterpret_cast<float4 *>(m[u].ch)[j] = q[j];
+                }
+            }
 #pragma unroll
         for (int u = 0; u < BATCH; ++u)
+            if (u < n)
 #pragma unroll
-            for (int i = 0; i < W; ++i) c[i] = m[u][i].x < 0.f ? m[u][i].y : fmaf(m[u][i].x, c[i], m[u][i].y);
+                for (int i = 0; i < W; ++i) c[i] = m[u].ch[i].x < 0.f ? m[u].ch[i].y : fmaf(m[u].ch[i].x, c[i], m[u].ch[i].y);
         k += n * step;
     }
 }
@@ -121,13 +139,14 @@ __device__ __forceinline__ void step_fwd(const R &ring, int slot, int s, int r, 
     if (SIG) vmul(v, b, v);
 }
 
-template <typename T, bool AL, bool SIG>
+template <typename T, int G, int LB, bool SIG>
 __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ ScanParams p) {
-    using RN = ScanRing<T, AL, 2>;
-    constexpr int W = RN::W, S = kStageRows, ST = ring_stages(2), TC = walk_channels<T>();
+    using RN = ScanRing<T, G, LB, 2>;
+    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), TC = walk_channels<T, LB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, D = p.D, R = p.span.R, units = (D + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
+    const bool full = c0 + TC <= D;
     int b, e;
     piece_rows(p.cut, p.span, piece, b, e);
     const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, D, R), walk_tensor<T>(p.g, p.g_stride, c0, D, R)},
@@ -147,7 +166,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
     if (b >= e) return;
     Seq q = seq_of(p.span, b, lane);
     float h[W];
-    if (q.start < b) compose(p.cut.maps, piece_of(p.cut, p.span, q.start), piece, 1, c, D, h);
+    if (q.start < b) compose(lane_map<W>(p.cut, c), (long long)units * 32, piece_of(p.cut, p.span, q.start), piece, 1, h);
     else get_state(p.s0, q.n, c, D, h);
     // behind the last row of a sequence
     auto close = [&](int row) {
@@ -170,11 +189,17 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
             float a[W], v[W];
             step_fwd<T, SIG>(ring, slot, s, r + s, p.lb, a, v);
             vfma(a, h, v, h);
-            put_row<AL>(out + (long long)s * D, c, D, lane, h);
+            put_row<G>(out + (long long)s * D, c, D, lane, full, h);
         };
         if (min(q.end, e) >= r + S) {
+            float a[S][W], v[S][W];
 #pragma unroll
-            for (int s = 0; s < S; ++s) one(s);
+            for (int s = 0; s < S; ++s) step_fwd<T, SIG>(ring, slot, s, r + s, p.lb, a[s], v[s]);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                vfma(a[s], h, v[s], h);
+                put_row<G>(out + (long long)s * D, c, D, lane, full, h);
+            }
             if (q.end == r + S) close(r + S);
         } else {
             const int n = min(S, e - r);
@@ -191,10 +216,10 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
 }
 
 // The map of a piece whose last sequence goes on behind it, over that sequence's rows.
-template <typename T, bool AL, bool SIG>
+template <typename T, int G, int LB, bool SIG>
 __global__ void __launch_bounds__(32) scan_reduce_kernel(const __grid_constant__ ScanParams p) {
-    using RN = ScanRing<T, AL, 2>;
-    constexpr int W = RN::W, S = kStageRows, ST = ring_stages(2), TC = walk_channels<T>();
+    using RN = ScanRing<T, G, LB, 2>;
+    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), TC = walk_channels<T, LB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, D = p.D, R = p.span.R, units = (D + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
@@ -235,8 +260,14 @@ __global__ void __launch_bounds__(32) scan_reduce_kernel(const __grid_constant__
             vmul(A, a, A);
         };
         if (e >= r + S) {
+            float a[S][W], v[S][W];
 #pragma unroll
-            for (int s = 0; s < S; ++s) one(s);
+            for (int s = 0; s < S; ++s) step_fwd<T, SIG>(ring, slot, s, r + s, p.lb, a[s], v[s]);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                vfma(a[s], h, v[s], h);
+                vmul(A, a[s], A);
+            }
         } else {
 #pragma unroll 1
             for (int s = 0; s < e - r; ++s) one(s);
@@ -244,9 +275,10 @@ __global__ void __launch_bounds__(32) scan_reduce_kernel(const __grid_constant__
         next = slot;
         slot = slot + 1 == ST ? 0 : slot + 1;
     }
+    Map<W> m;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-        if (c + i < D) p.cut.maps[(long long)piece * D + c + i] = make_float2(begins ? -1.f : A[i], h[i]);
+    for (int i = 0; i < W; ++i) m.ch[i] = make_float2(begins ? -1.f : A[i], h[i]);
+    lane_map<W>(p.cut, c)[(long long)piece * units * 32] = m;
 }
 
 // ---------------------------------------------------------------- backward
@@ -256,14 +288,15 @@ __global__ void __launch_bounds__(32) scan_reduce_kernel(const __grid_constant__
 // The same walk from the last row to the first; h is the forward's output, so h_{t-1}
 // carries the rounding of its type (half a step, as the gradient itself does), which saves
 // the forward's recomputation and the reading of x in the log form.
-template <typename T, bool AL, bool SIG>
+template <typename T, int G, int LB, bool SIG>
 __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ ScanBwdParams p) {
     constexpr int N = SIG ? 4 : 3;
-    using RN = ScanRing<T, AL, N>;
-    constexpr int W = RN::W, S = kStageRows, ST = ring_stages(N), TC = walk_channels<T>();
+    using RN = ScanRing<T, G, LB, N>;
+    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, N), TC = walk_channels<T, LB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, D = p.D, R = p.span.R, units = (D + TC - 1) / TC;
     const int place = blockIdx.x / units, piece = p.cut.pieces - 1 - place, c0 = (blockIdx.x - place * units) * TC, c = c0 + lane * W;
+    const bool full = c0 + TC <= D;
     int b, e;
     piece_rows(p.cut, p.span, piece, b, e);
     RN ring{dyn, {walk_tensor<T>(p.g, p.g_stride, c0, D, R), walk_tensor<T>(p.dout, p.dout_stride, c0, D, R),
@@ -287,7 +320,7 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
     if (b >= e) return;
     Seq q = seq_of(p.span, e - 1, lane);
     float k[W];
-    if (q.end > e) compose(p.cut.maps, piece_of(p.cut, p.span, q.end - 1), piece, -1, c, D, k);
+    if (q.end > e) compose(lane_map<W>(p.cut, c), (long long)units * 32, piece_of(p.cut, p.span, q.end - 1), piece, -1, k);
     else get_state(p.dsT, q.n, c, D, k);
     int slot = 0, next = ST - 1;
 #pragma unroll 1
@@ -321,8 +354,8 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
                 for (int i = 0; i < W; ++i)
                     if (g[i] < p.lb) dg[i] = 0.f;
             }
-            put_row<AL>(static_cast<T *>(p.dx) + (long long)row * D, c, D, lane, d);
-            put_row<AL>(static_cast<T *>(p.dg) + (long long)row * D, c, D, lane, dg);
+            put_row<G>(static_cast<T *>(p.dx) + (long long)row * D, c, D, lane, full, d);
+            put_row<G>(static_cast<T *>(p.dg) + (long long)row * D, c, D, lane, full, dg);
         };
         if (r >= b && q.start < r) {
 #pragma unroll
@@ -347,10 +380,10 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
 }
 
 // The map, run backwards, of a piece whose first sequence began before it.
-template <typename T, bool AL, bool SIG>
+template <typename T, int G, int LB, bool SIG>
 __global__ void __launch_bounds__(32) scan_reduce_bwd_kernel(const __grid_constant__ ScanBwdParams p) {
-    using RN = ScanRing<T, AL, 2>;
-    constexpr int W = RN::W, S = kStageRows, ST = ring_stages(2), TC = walk_channels<T>();
+    using RN = ScanRing<T, G, LB, 2>;
+    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), TC = walk_channels<T, LB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, D = p.D, R = p.span.R, units = (D + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
@@ -404,9 +437,10 @@ __global__ void __launch_bounds__(32) scan_reduce_bwd_kernel(const __grid_consta
         next = slot;
         slot = slot + 1 == ST ? 0 : slot + 1;
     }
+    Map<W> m;
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-        if (c + i < D) p.cut.maps[(long long)piece * D + c + i] = make_float2(ends ? -1.f : A[i], h[i]);
+    for (int i = 0; i < W; ++i) m.ch[i] = make_float2(ends ? -1.f : A[i], h[i]);
+    lane_map<W>(p.cut, c)[(long long)piece * units * 32] = m;
 }
 
 // ---------------------------------------------------------------- single token
@@ -447,26 +481,28 @@ __global__ void __launch_bounds__(128) scan_step_kernel(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- host
-int units_of(int D, bool bf16) {
-    const int tc = bf16 ? walk_channels<__nv_bfloat16>() : walk_channels<float>();
+int units_of(int D, bool bf16, int lb) {
+    const int tc = bf16 ? 16 * lb : 8 * lb;
     return (D + tc - 1) / tc;
 }
 
-// How the rows are cut. Whole sequences where walkers of whole sequences come to half of
-// those that can run at a time, none more than three times as long as the average (one
-// pass; without the lengths on the host a packed batch is taken to be ragged); otherwise
-// pieces of equal length, for one full wave of walkers and of 128 rows at least.
-ScanCut scan_cut(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16) {
-    const int units = units_of(D, bf16);
+// How the rows are cut for walkers of `lb` bytes a lane. Whole sequences where walkers of
+// whole sequences come to half of those that can run at a time, none more than three times
+// as long as the average (one pass; without the lengths on the host a packed batch is taken
+// to be ragged); otherwise pieces of equal length, for one full wave of walkers and of
+// kMinPiece rows at least.
+ScanCut cut_for(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int lb) {
+    const int units = units_of(D, bf16, lb);
     const long long want = kWalkerSlots > units ? kWalkerSlots / units : 1;  // pieces of a full wave
     ScanCut c{};
+    c.lb = lb;
     if (sp.R == 0) {
         c.kind = kCutRows; c.pieces = 1; c.rows = 1;
         return c;
     }
-    auto stages = [](long long rows) { return (int)((rows + kStageRows - 1) / kStageRows * kStageRows); };
+    auto stages = [](long long rows) { return (int)((rows + kStage - 1) / kStage * kStage); };
     if (!sp.cu) {
-        if (2LL * sp.N >= want || sp.T <= 128) {
+        if (2LL * sp.N >= want || sp.T <= 2 * kMinPiece) {
             // whole sequences, several to a walker where there are many
             const long long each = (sp.N + want - 1) / want;
             c.kind = kCutRows;
@@ -474,9 +510,9 @@ ScanCut scan_cut(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16) {
             c.pieces = (int)((sp.N + each - 1) / each);
             return c;
         }
-        const int per = (int)((want + sp.N - 1) / sp.N);
+        const int per = (int)(want / sp.N);
         c.kind = kCutBatch;
-        c.rows = stages(sp.T / per > 128 ? (sp.T + per - 1) / per : 128);
+        c.rows = stages(sp.T / per > kMinPiece ? (sp.T + per - 1) / per : kMinPiece);
         c.per = (sp.T + c.rows - 1) / c.rows;
         c.pieces = sp.N * c.per;
         c.carries = c.per > 1;
@@ -485,37 +521,58 @@ ScanCut scan_cut(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16) {
     if (cu_host && 2LL * sp.N >= want && sp.N <= 4 * want) {
         int longest = 0;
         for (int n = 0; n < sp.N; ++n) longest = longest < cu_host[n + 1] - cu_host[n] ? cu_host[n + 1] - cu_host[n] : longest;
-        if ((long long)longest * sp.N <= 3LL * sp.R || longest <= 128) {
+        if ((long long)longest * sp.N <= 3LL * sp.R || longest <= 2 * kMinPiece) {
             c.kind = kCutSeqs; c.pieces = sp.N;
             return c;
         }
     }
     c.kind = kCutRows;
-    c.rows = stages(sp.R / want > 128 ? (sp.R + want - 1) / want : 128);
+    c.rows = stages(sp.R / want > kMinPiece ? (sp.R + want - 1) / want : kMinPiece);
     c.pieces = (sp.R + c.rows - 1) / c.rows;
     c.carries = c.pieces > 1;
     return c;
 }
 
+// Lanes of 8 bytes take about two thirds of the instructions an element; lanes of 4 make
+// twice the walkers, and are taken where they save the cut along time (31744 x 12288 packed
+// of four sequences: 490 us in one pass, against 637 with lanes of 8 in two).
+ScanCut scan_cut(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int g) {
+    const ScanCut wide = cut_for(sp, cu_host, D, bf16, 8);
+    if (!wide.carries || g < 16) return wide;
+    const ScanCut narrow = cut_for(sp, cu_host, D, bf16, 4);
+    return narrow.carries ? wide : narrow;
+}
+
 // Launches a walker for each piece and channel unit.
 template <typename T, typename P> cudaError_t run_walk(void (*kernel)(P), const P &p, int ring_bytes, cudaStream_t st) {
-    const long long grid = (long long)p.cut.pieces * units_of(p.D, sizeof(T) == 2);
+    const long long grid = (long long)p.cut.pieces * units_of(p.D, sizeof(T) == 2, p.cut.lb);
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     count_launch();
     kernel<<<(unsigned)grid, 32, ring_bytes, st>>>(p);
     return cudaGetLastError();
 }
 
-template <typename T, bool AL, bool SIG> cudaError_t run_fwd(const ScanParams &p, cudaStream_t st) {
-    constexpr int ring = ScanRing<T, AL, 2>::BYTES;
+template <typename T, int G, int LB, bool SIG> cudaError_t run_fwd_lb(const ScanParams &p, cudaStream_t st) {
+    constexpr int ring = ScanRing<T, G, LB, 2>::BYTES;
     cudaError_t e = cudaSuccess;
-    if (p.cut.carries) e = run_walk<T>(scan_reduce_kernel<T, AL, SIG>, p, ring, st);
-    return e != cudaSuccess ? e : run_walk<T>(scan_fwd_kernel<T, AL, SIG>, p, ring, st);
+    if (p.cut.carries) e = run_walk<T>(scan_reduce_kernel<T, G, LB, SIG>, p, ring, st);
+    return e != cudaSuccess ? e : run_walk<T>(scan_fwd_kernel<T, G, LB, SIG>, p, ring, st);
 }
-template <typename T, bool AL, bool SIG> cudaError_t run_bwd(const ScanBwdParams &p, cudaStream_t st) {
+template <typename T, int G, int LB, bool SIG> cudaError_t run_bwd_lb(const ScanBwdParams &p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.cut.carries) e = run_walk<T>(scan_reduce_bwd_kernel<T, AL, SIG>, p, ScanRing<T, AL, 2>::BYTES, st);
-    return e != cudaSuccess ? e : run_walk<T>(scan_bwd_kernel<T, AL, SIG>, p, ScanRing<T, AL, SIG ? 4 : 3>::BYTES, st);
+    if (p.cut.carries) e = run_walk<T>(scan_reduce_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, 2>::BYTES, st);
+    return e != cudaSuccess ? e : run_walk<T>(scan_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, SIG ? 4 : 3>::BYTES, st);
+}
+// Lanes of 4 bytes come with 16-byte accesses only (see scan_cut).
+template <typename T, int G, bool SIG> cudaError_t run_fwd(const ScanParams &p, cudaStream_t st) {
+    if constexpr (G == 16)
+        if (p.cut.lb == 4) return run_fwd_lb<T, G, 4, SIG>(p, st);
+    return run_fwd_lb<T, G, 8, SIG>(p, st);
+}
+template <typename T, int G, bool SIG> cudaError_t run_bwd(const ScanBwdParams &p, cudaStream_t st) {
+    if constexpr (G == 16)
+        if (p.cut.lb == 4) return run_bwd_lb<T, G, 4, SIG>(p, st);
+    return run_bwd_lb<T, G, 8, SIG>(p, st);
 }
 template <typename T, bool AL, bool SIG> cudaError_t run_step(const ScanStepParams &p, cudaStream_t st) {
     const long long threads = (long long)p.N * (p.D / (AL ? 4 : 1));
@@ -524,54 +581,66 @@ template <typename T, bool AL, bool SIG> cudaError_t run_step(const ScanStepPara
     return cudaGetLastError();
 }
 
-// Runs F<T, AL, SIG> for the types and layouts of a call.
-#define KDA_SCAN_PICK(F, p, bf16, al, sig, st)                                                                                          \
-    return bf16 ? (al ? (sig ? F<__nv_bfloat16, true, true>(p, st) : F<__nv_bfloat16, true, false>(p, st))                              \
-                      : (sig ? F<__nv_bfloat16, false, true>(p, st) : F<__nv_bfloat16, false, false>(p, st)))                           \
-                : (al ? (sig ? F<float, true, true>(p, st) : F<float, true, false>(p, st))                                              \
-                      : (sig ? F<float, false, true>(p, st) : F<float, false, false>(p, st)));
+// Runs F<T, G, SIG> for the types and layouts of a call.
+#define KDA_SCAN_SIG(F, T, G, sig) return sig ? F<T, G, true>(p, st) : F<T, G, false>(p, st);
+#define KDA_SCAN_PICK(F, p, bf16, g, sig, st)                    \
+    if (bf16) {                                                  \
+        if (g == 16) KDA_SCAN_SIG(F, __nv_bfloat16, 16, sig)     \
+        if (g == 8) KDA_SCAN_SIG(F, __nv_bfloat16, 8, sig)       \
+        if (g == 4) KDA_SCAN_SIG(F, __nv_bfloat16, 4, sig)       \
+        KDA_SCAN_SIG(F, __nv_bfloat16, 2, sig)                   \
+    }                                                            \
+    if (g == 16) KDA_SCAN_SIG(F, float, 16, sig)                 \
+    if (g == 8) KDA_SCAN_SIG(F, float, 8, sig)                   \
+    KDA_SCAN_SIG(F, float, 4, sig)
 
 }  // namespace
 
 size_t scan_workspace_bytes(const RowSpan &span, const int32_t *cu_host, int D, bool bf16) {
-    const ScanCut c = scan_cut(span, cu_host, D, bf16);
-    return c.carries ? sizeof(float2) * (size_t)c.pieces * D : 0;
+    // of the wider walkers: whether the narrower are taken goes by alignment too
+    const ScanCut c = cut_for(span, cu_host, D, bf16, 8);
+    return c.carries ? sizeof(float2) * (size_t)c.pieces * units_of(D, bf16, 8) * (bf16 ? 128 : 64) : 0;
 }
 
 cudaError_t launch_scan(ScanParams p, const int32_t *cu_host, bool bf16, bool sigmoid, void *workspace, cudaStream_t st) {
-    p.cut = scan_cut(p.span, cu_host, p.D, bf16);
-    p.cut.maps = static_cast<float2 *>(workspace);
     const size_t esz = bf16 ? 2 : 4;
-    Aligned al;
-    al.rows(p.x, p.x_stride, p.D, esz);
-    al.rows(p.g, p.g_stride, p.D, esz);
-    al.rows(p.h, p.D, p.D, esz);
-    KDA_SCAN_PICK(run_fwd, p, bf16, al.ok, sigmoid, st)
+    RowAccess ac;
+    ac.rows(p.x, p.x_stride, p.D, esz);
+    ac.rows(p.g, p.g_stride, p.D, esz);
+    ac.rows(p.h, p.D, p.D, esz);
+    p.cut = scan_cut(p.span, cu_host, p.D, bf16, ac.g());
+    p.cut.maps = workspace;
+    KDA_SCAN_PICK(run_fwd, p, bf16, ac.g(), sigmoid, st)
 }
 
 cudaError_t launch_scan_bwd(ScanBwdParams p, const int32_t *cu_host, bool bf16, bool sigmoid, void *workspace, cudaStream_t st) {
-    p.cut = scan_cut(p.span, cu_host, p.D, bf16);
-    p.cut.maps = static_cast<float2 *>(workspace);
     const size_t esz = bf16 ? 2 : 4;
-    Aligned al;
-    if (sigmoid) al.rows(p.x, p.x_stride, p.D, esz);
-    al.rows(p.g, p.g_stride, p.D, esz);
-    al.rows(p.h, p.h_stride, p.D, esz);
-    al.rows(p.dout, p.dout_stride, p.D, esz);
-    al.rows(p.dx, p.D, p.D, esz);
-    al.rows(p.dg, p.D, p.D, esz);
-    KDA_SCAN_PICK(run_bwd, p, bf16, al.ok, sigmoid, st)
+    RowAccess ac;
+    if (sigmoid) ac.rows(p.x, p.x_stride, p.D, esz);
+    ac.rows(p.g, p.g_stride, p.D, esz);
+    ac.rows(p.h, p.h_stride, p.D, esz);
+    ac.rows(p.dout, p.dout_stride, p.D, esz);
+    ac.rows(p.dx, p.D, p.D, esz);
+    ac.rows(p.dg, p.D, p.D, esz);
+    p.cut = scan_cut(p.span, cu_host, p.D, bf16, ac.g());
+    p.cut.maps = workspace;
+    KDA_SCAN_PICK(run_bwd, p, bf16, ac.g(), sigmoid, st)
 }
 
 cudaError_t launch_scan_step(const ScanStepParams &p, bool bf16, bool sigmoid, cudaStream_t st) {
     const size_t esz = bf16 ? 2 : 4;
-    Aligned al;
-    al.rows(p.x, p.x_stride, p.D, esz);
-    al.rows(p.g, p.g_stride, p.D, esz);
-    al.rows(p.h, p.D, p.D, esz);
-    al.rows(p.state, p.D, p.D, 4);
-    al.rows(p.state_out, p.D, p.D, 4);
-    KDA_SCAN_PICK(run_step, p, bf16, al.ok, sigmoid, st)
+    RowAccess ac;
+    ac.rows(p.x, p.x_stride, p.D, esz);
+    ac.rows(p.g, p.g_stride, p.D, esz);
+    ac.rows(p.h, p.D, p.D, esz);
+    ac.rows(p.state, p.D, p.D, 4);
+    ac.rows(p.state_out, p.D, p.D, 4);
+    if (bf16) {
+        if (ac.g() == 16) return sigmoid ? run_step<__nv_bfloat16, true, true>(p, st) : run_step<__nv_bfloat16, true, false>(p, st);
+        return sigmoid ? run_step<__nv_bfloat16, false, true>(p, st) : run_step<__nv_bfloat16, false, false>(p, st);
+    }
+    if (ac.g() == 16) return sigmoid ? run_step<float, true, true>(p, st) : run_step<float, true, false>(p, st);
+    return sigmoid ? run_step<float, false, true>(p, st) : run_step<float, false, false>(p, st);
 }
 
 }  // namespace kda

@@ -1,9 +1,10 @@
 // Walkers: how the operators that run along time over packed [rows, channels] tensors cut
-// and read them. A walker is one warp (and one CTA) that walks 128 bytes of channels -- 64
-// in bf16, 32 in fp32, 4 bytes a lane -- down a piece of the rows, with what it carries in
-// registers. Asynchronous copies run stages of 16 rows ahead of it into a ring in its own
-// shared memory, so no barrier and no other warp is involved, every element is read once,
-// and the walkers of an SM keep some 170 KB of reads in flight between them.
+// and read them. A walker is one warp (and one CTA) that walks 32 LB bytes of channels (LB =
+// 4 or 8 bytes a lane: 64 or 128 channels in bf16, half of that in fp32) down a piece of the
+// rows, with what it carries in registers. Asynchronous copies run stages of rows ahead of
+// it into a ring in its own shared memory, so no barrier and no other warp is involved,
+// every element is read once, and the walkers of an SM keep some 170 KB of reads in flight
+// between them.
 #pragma once
 
 #include "kda_common.cuh"
@@ -18,12 +19,9 @@ struct RowSpan {
     int T, N, R;
 };
 
-constexpr int kStageRows = 16;
-constexpr int kWalkBytes = 128;
-
-// Channels of a walker, and of a lane.
-template <typename T> constexpr int walk_channels() { return kWalkBytes / (int)sizeof(T); }
-template <typename T> constexpr int lane_channels() { return 4 / (int)sizeof(T); }
+// Channels of a lane, and of a walker.
+template <typename T, int LB> constexpr int lane_channels() { return LB / (int)sizeof(T); }
+template <typename T, int LB> constexpr int walk_channels() { return 32 * lane_channels<T, LB>(); }
 
 // ---------------------------------------------------------------- arithmetic
 // The SFU's exponential (off by 2 steps) and reciprocal (1 step), for bf16 results.
@@ -51,30 +49,71 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // d = a b + c, d = a b, d = a + b of a lane's channels: one instruction for two.
-__device__ __forceinline__ void vfma(const float (&a)[1], const float (&b)[1], const float (&c)[1], float (&d)[1]) { d[0] = fmaf(a[0], b[0], c[0]); }
-__device__ __forceinline__ void vmul(const float (&a)[1], const float (&b)[1], float (&d)[1]) { d[0] = a[0] * b[0]; }
-__device__ __forceinline__ void vadd(const float (&a)[1], const float (&b)[1], float (&d)[1]) { d[0] = a[0] + b[0]; }
-__device__ __forceinline__ void vfma(const float (&a)[2], const float (&b)[2], const float (&c)[2], float (&d)[2]) {
+__device__ __forceinline__ void pair_fma(const float *a, const float *b, const float *c, float *d) {
     asm("{\n\t.reg .b64 ra, rb, rc;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
         "fma.rn.f32x2 rc, ra, rb, rc;\n\tmov.b64 {%0, %1}, rc;\n\t}"
         : "=f"(d[0]), "=f"(d[1])
         : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]), "f"(c[0]), "f"(c[1]));
 }
-__device__ __forceinline__ void vmul(const float (&a)[2], const float (&b)[2], float (&d)[2]) {
+__device__ __forceinline__ void pair_mul(const float *a, const float *b, float *d) {
     asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
         "mul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
         : "=f"(d[0]), "=f"(d[1])
         : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
 }
-__device__ __forceinline__ void vadd(const float (&a)[2], const float (&b)[2], float (&d)[2]) {
+__device__ __forceinline__ void pair_add(const float *a, const float *b, float *d) {
     asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
         "add.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
         : "=f"(d[0]), "=f"(d[1])
         : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
 }
+template <int W> __device__ __forceinline__ void vfma(const float (&a)[W], const float (&b)[W], const float (&c)[W], float (&d)[W]) {
+    if constexpr (W == 1) {
+        d[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 2) pair_fma(a + i, b + i, c + i, d + i);
+    }
+}
+template <int W> __device__ __forceinline__ void vmul(const float (&a)[W], const float (&b)[W], float (&d)[W]) {
+    if constexpr (W == 1) {
+        d[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 2) pair_mul(a + i, b + i, d + i);
+    }
+}
+template <int W> __device__ __forceinline__ void vadd(const float (&a)[W], const float (&b)[W], float (&d)[W]) {
+    if constexpr (W == 1) {
+        d[0] = a[0] + b[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 2) pair_add(a + i, b + i, d + i);
+    }
+}
 template <int W> __device__ __forceinline__ void vset(float (&d)[W], float v) {
 #pragma unroll
     for (int i = 0; i < W; ++i) d[i] = v;
+}
+
+// The sum of column `col` over `slices` rows of `cols` partial sums, by a CTA of 32 warps:
+// each warp adds its share in order, then the warps' sums are added in order. The result is
+// the first warp's, whose lanes hold 32 neighbouring columns.
+__device__ __forceinline__ float slice_sum(const float *partial, int slices, long long cols, long long col) {
+    __shared__ float red[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float s = 0.f;
+    if (col < cols) {
+#pragma unroll 8
+        for (int j = warp; j < slices; j += 32) s += partial[j * cols + col];
+    }
+    red[warp][lane] = s;
+    __syncthreads();
+    float v = 0.f;
+    if (warp == 0)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v += red[j][lane];
+    return v;
 }
 
 // ---------------------------------------------------------------- staged rows
@@ -92,108 +131,166 @@ __device__ __forceinline__ WalkTensor walk_tensor(const void *base, long long st
             b + ((long long)(R - 1) * stride + C) * (long long)sizeof(T)};
 }
 
-// The ring of a walker: STAGES stages of 16 rows of N tensors. AL: rows and base are
-// 16-byte aligned. Otherwise a row is copied with the 16-byte words that hold it (those
-// that reach beyond the tensor element by element) and read at its offset in them, so odd
-// widths and odd slices move the same bytes in almost as few instructions.
-template <typename T, bool AL, int N, int STAGES> struct Ring {
-    static constexpr int W = lane_channels<T>();
-    static constexpr int PITCH = AL ? kWalkBytes : kWalkBytes + 16, PART = kStageRows * PITCH, BYTES = STAGES * N * PART;
-    static constexpr int WORDS = PITCH / 16;
+// The lane's channels of a row as stored, and unpacked.
+template <int LB> struct Raw {
+    uint32_t w[LB / 4];
+};
+template <typename T, int LB> __device__ __forceinline__ void unpack(const Raw<LB> &r, float (&v)[lane_channels<T, LB>()]) {
+#pragma unroll
+    for (int i = 0; i < LB / 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            v[i] = __uint_as_float(r.w[i]);
+        } else {
+            v[2 * i] = __uint_as_float(r.w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// How rows are accessed: by G bytes at a time, G the largest of 16, 8, 4 and 2 that divides
+// the base, the row stride and the row's length of all the tensors of a call.
+struct RowAccess {
+    unsigned long long bits = 0;
+    void rows(const void *p, long long stride, long long C, size_t esz) {
+        if (p) bits |= reinterpret_cast<uintptr_t>(p) | (unsigned long long)stride * esz | (unsigned long long)C * esz;
+    }
+    int g() const { return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2; }
+};
+
+// The ring of a walker: STAGES stages of S rows of N tensors. Rows of 16-, 8- or 4-byte
+// aligned elements are copied to where a lane reads its LB bytes at once. Rows of single
+// bf16 elements (G = 2: odd widths) are copied with the 16-byte words that hold them -- those
+// that reach beyond the tensor element by element -- and read at their offset in those.
+template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
+    static constexpr int W = lane_channels<T, LB>(), ROW = 32 * LB;
+    static constexpr bool WHOLE = G > 2;  // rows are copied to where lanes read them
+    static constexpr int PITCH = WHOLE ? ROW : ROW + 16, PART = S * PITCH, BYTES = STAGES * N * PART;
     char *base;
     WalkTensor t[N];
     int width;  // bytes of a row that are the walker's
     int lane;
 
-    // Starts the copies of rows row .. row+15 of tensor i into stage `slot`: those in [lo, hi).
+    template <int B> static __device__ __forceinline__ void copy(unsigned to, const char *from) {
+        if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(B) : "memory");
+    }
+
+    // Starts the copies of rows row .. row+S-1 of tensor i into stage `slot`: those in [lo, hi).
     __device__ __forceinline__ void load(int slot, int i, int row, int lo, int hi) const {
         char *to = base + (slot * N + i) * PART;
-        if (AL) {
-            const int lr = lane >> 3, lc = (lane & 7) * 16;
+        const bool inner = row >= lo && row + S <= hi;
+        if constexpr (WHOLE) {
+            constexpr int PER = ROW / G;  // copies of a row
+            constexpr int ROWS = PER < 32 ? 32 / PER : 1, ROUNDS = PER < 32 ? 1 : PER / 32;
+            static_assert(S % ROWS == 0, "whole rounds");
+            const int lr = PER < 32 ? lane / PER : 0, lc = (PER < 32 ? lane % PER : lane) * G;
             const char *src = t[i].at + (long long)(row + lr) * t[i].stride + lc;
-            unsigned d = (unsigned)__cvta_generic_to_shared(to + lr * PITCH + lc);
+            const unsigned d = (unsigned)__cvta_generic_to_shared(to + lr * PITCH + lc);
+            const long long step = ROWS * t[i].stride;
+            if (inner && width == ROW) {
 #pragma unroll
-            for (int k = 0; k < kStageRows; k += 4) {
-                const int r = row + lr + k;
-                if (r >= lo && r < hi && lc < width)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + k * PITCH), "l"(src + k * t[i].stride) : "memory");
+                for (int k = 0; k < S; k += ROWS, src += step)
+#pragma unroll
+                    for (int j = 0; j < ROUNDS; ++j) copy<G>(d + k * PITCH + j * 32 * G, src + j * 32 * G);
+                return;
             }
-            return;
-        }
+#pragma unroll 1
+            for (int k = 0; k < S; k += ROWS, src += step) {
+                const int r = row + lr + k;
+                if (r >= lo && r < hi)
 #pragma unroll
-        for (int q = 0; q < (kStageRows * WORDS + 31) / 32; ++q) {
-            const int x = q * 32 + lane, k = x / WORDS, j = x - k * WORDS, r = row + k;
-            if (k < kStageRows && r >= lo && r < hi) {
+                    for (int j = 0; j < ROUNDS; ++j)
+                        if (lc + j * 32 * G < width) copy<G>(d + k * PITCH + j * 32 * G, src + j * 32 * G);
+            }
+        } else {
+            constexpr int WORDS = PITCH / 16, COUNT = S * WORDS;
+            // only words of the tensor's first and last rows may reach beyond it
+            const bool plain = row > lo && row + S < hi && width == ROW;
+            if (plain) {
+#pragma unroll
+                for (int q = 0; q < (COUNT + 31) / 32; ++q) {
+                    const int x = q * 32 + lane, k = x / WORDS, j = x - k * WORDS;
+                    const char *a = t[i].at + (long long)(row + k) * t[i].stride;
+                    const int off = (int)((uint32_t)reinterpret_cast<uintptr_t>(a) & 15u);
+                    // the last word of a row that begins on a boundary is none of its
+                    if (x < COUNT && (j < WORDS - 1 || off)) copy<16>((unsigned)__cvta_generic_to_shared(to + x * 16), a - off + 16 * j);
+                }
+                return;
+            }
+#pragma unroll 1
+            for (int x = lane; x < COUNT; x += 32) {
+                const int k = x / WORDS, j = x - k * WORDS, r = row + k;
+                if (r < lo || r >= hi) continue;
                 const char *a = t[i].at + (long long)r * t[i].stride;
-                const char *w = a - (reinterpret_cast<uintptr_t>(a) & 15) + 16 * j;
-                if (w < a + width) {
-                    if (w >= t[i].begin && w + 16 <= t[i].end) {
-                        const unsigned d = (unsigned)__cvta_generic_to_shared(to + k * PITCH + 16 * j);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(w) : "memory");
-                    } else {
-                        for (int b = 0; b < 16; b += (int)sizeof(T))
-                            if (w + b >= a && w + b < a + width)
-                                *reinterpret_cast<T *>(to + k * PITCH + 16 * j + b) = *reinterpret_cast<const T *>(w + b);
-                    }
+                const int off = (int)((uint32_t)reinterpret_cast<uintptr_t>(a) & 15u);
+                const char *w = a - off + 16 * j;
+                if (16 * j - off >= width) continue;
+                if (w >= t[i].begin && w + 16 <= t[i].end) {
+                    copy<16>((unsigned)__cvta_generic_to_shared(to + x * 16), w);
+                } else {
+                    for (int e = 0; e < 16; e += (int)sizeof(T))
+                        if (16 * j - off + e >= 0 && 16 * j - off + e < width)
+                            *reinterpret_cast<T *>(to + x * 16 + e) = *reinterpret_cast<const T *>(w + e);
                 }
             }
         }
     }
     // The lane's channels of row r, the s-th of stage `slot`.
-    __device__ __forceinline__ void get(int slot, int i, int s, int r, float (&v)[W]) const {
-        const char *p = base + (slot * N + i) * PART + s * PITCH + lane * 4;
-        uint32_t q;
-        if (AL) {
-            q = *reinterpret_cast<const uint32_t *>(p);
+    __device__ __forceinline__ Raw<LB> raw(int slot, int i, int s, int r) const {
+        const char *p = base + (slot * N + i) * PART + s * PITCH + lane * LB;
+        Raw<LB> q;
+        if constexpr (WHOLE) {
+            if constexpr (LB == 4) q.w[0] = *reinterpret_cast<const uint32_t *>(p);
+            else reinterpret_cast<uint2 &>(q) = *reinterpret_cast<const uint2 *>(p);
         } else {
             const uint32_t shift = ((uint32_t)reinterpret_cast<uintptr_t>(t[i].at) + (uint32_t)r * (uint32_t)t[i].stride) & 15u;
             const uint32_t *w = reinterpret_cast<const uint32_t *>(p + (shift & 12u));
-            q = w[0];
-            if (sizeof(T) == 2) q = __funnelshift_r(q, w[1], (shift & 2u) * 8u);
+#pragma unroll
+            for (int j = 0; j < LB / 4; ++j) q.w[j] = __funnelshift_r(w[j], w[j + 1], shift * 8u & 16u);
         }
-        if constexpr (W == 1) {
-            v[0] = __uint_as_float(q);
-        } else {
-            v[0] = __uint_as_float(q << 16);
-            v[1] = __uint_as_float(q & 0xffff0000u);
-        }
+        return q;
     }
+    __device__ __forceinline__ void get(int slot, int i, int s, int r, float (&v)[W]) const { unpack<T, LB>(raw(slot, i, s, r), v); }
 };
 
 // Stores the lane's channels, from c on, of an output row (the whole warp takes part).
-template <bool AL> __device__ __forceinline__ void put_row(float *row, int c, int C, int, const float (&v)[1]) {
-    if (c < C) row[c] = v[0];
-}
-template <bool AL> __device__ __forceinline__ void put_row(__nv_bfloat16 *row, int c, int C, int lane, const float (&v)[2]) {
-    if (AL) {
-        if (c < C) *reinterpret_cast<uint32_t *>(row + c) = pack_bf16(v[0], v[1]);
-        return;
-    }
-    if (reinterpret_cast<uintptr_t>(row) & 2) {
-        // the row begins in the middle of a word: words pair a lane's second channel with the next lane's first
-        const float before = __shfl_up_sync(0xffffffffu, v[1], 1);
-        if (lane == 0) {
-            if (c < C) row[c] = __float2bfloat16_rn(v[0]);
-        } else if (c < C) {
-            *reinterpret_cast<uint32_t *>(row + c - 1) = pack_bf16(before, v[0]);
-        } else if (c - 1 < C) {
-            row[c - 1] = __float2bfloat16_rn(before);
-        }
-        if (lane == 31 && c + 1 < C) row[c + 1] = __float2bfloat16_rn(v[1]);
-    } else if (c + 1 < C) {
-        *reinterpret_cast<uint32_t *>(row + c) = pack_bf16(v[0], v[1]);
-    } else if (c < C) {
-        row[c] = __float2bfloat16_rn(v[0]);
+// full: all the channels of the walker are below C.
+template <int G, int W> __device__ __forceinline__ void put_row(float *row, int c, int C, int, bool, const float (&v)[W]) {
+    if constexpr (G >= 8 && W == 2) {
+        if (c < C) *reinterpret_cast<float2 *>(row + c) = make_float2(v[0], v[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (c + i < C) row[c + i] = v[i];
     }
 }
-
-// Whether all the tensors of a call have 16-byte aligned rows.
-struct Aligned {
-    bool ok = true;
-    void rows(const void *p, long long stride, long long C, size_t esz) {
-        if (p && ((reinterpret_cast<uintptr_t>(p) | (unsigned long long)stride * esz | (unsigned long long)C * esz) & 15)) ok = false;
+template <int G, int W> __device__ __forceinline__ void put_row(__nv_bfloat16 *row, int c, int C, int lane, bool full, const float (&v)[W]) {
+    if constexpr (G >= 8 && W == 4) {
+        if (c < C) *reinterpret_cast<uint2 *>(row + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    } else if constexpr (G >= 4) {
+#pragma unroll
+        for (int i = 0; i < W; i += 2)
+            if (c + i < C) *reinterpret_cast<uint32_t *>(row + c + i) = pack_bf16(v[i], v[i + 1]);
+    } else if (!full) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (c + i < C) row[c + i] = __float2bfloat16_rn(v[i]);
+    } else {
+        // where the row begins in the middle of a word, words pair a lane's last channel with the next lane's first
+        const bool odd = reinterpret_cast<uintptr_t>(row) & 2;
+        float x[W];
+        x[0] = __shfl_up_sync(0xffffffffu, v[W - 1], 1);
+#pragma unroll
+        for (int i = W - 1; i > 0; --i) x[i] = odd ? v[i - 1] : v[i];
+        if (!odd) x[0] = v[0];
+        uint32_t *w = reinterpret_cast<uint32_t *>(row + (odd ? c - 1 : c));
+#pragma unroll
+        for (int i = 0; i < W; i += 2)
+            if (i > 0 || lane > 0 || !odd) w[i / 2] = pack_bf16(x[i], x[i + 1]);
+        if (odd && lane == 0) row[c] = __float2bfloat16_rn(v[0]);
+        if (odd && lane == 31) row[c + W - 1] = __float2bfloat16_rn(v[W - 1]);
     }
-};
+}
 
 // ---------------------------------------------------------------- rows and sequences
 // First i in [0, n] with a[i] >= v of n non-decreasing values, by one warp: 32 probes a

@@ -181,6 +181,8 @@ def _norm_args(x, weight, residual, gate, eps, residual_out):
     stride = _act("x", x, x)
     a = _abi.RMSNormArgs(dtype=dt, rows=rows, D=D, x=_ptr(x), x_stride=stride, eps=eps)
     a.weight, a.weight_dtype = _weight(weight, x)
+    if residual is not None and gate is not None:
+        raise ValueError("residual and gate cannot be combined")
     if residual is not None:
         a.residual_stride = _act("residual", residual, x)
         a.residual = _ptr(residual)
@@ -225,7 +227,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual
              gate: Optional[torch.Tensor] = None, eps: float = 1e-6, out: Optional[torch.Tensor] = None,
              residual_out: Optional[torch.Tensor] = None):
     """Root-mean-square norm over the last dimension:
-    ``s = x (+ residual)``, ``y = s / sqrt(mean(s^2) + eps) * weight * sigmoid(gate)``.
+    ``s = x (+ residual)``, ``y = s / sqrt(mean(s^2) + eps) * weight * sigmoid(gate)``
+    (a residual or a gate, not both).
 
     x, residual, gate: [..., D] float32 or bfloat16, D up to 16384; weight: [D] float32 or x's
     dtype, or None. ``gate`` is the output gate of a KDA layer (page
@@ -281,6 +284,8 @@ def rms_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.Tenso
                             dy_stride=_act("dy", dy, x), dy=_ptr(dy), eps=eps)
     a.weight, a.weight_dtype = _weight(weight, x)
     dgate = dw = None
+    if gate is not None and dresidual is not None:
+        raise ValueError("dresidual and gate cannot be combined")
     if gate is not None:
         a.gate_stride = _act("gate", gate, x)
         a.gate = _ptr(gate)

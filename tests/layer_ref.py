@@ -58,8 +58,9 @@ def norm_rel(D):
     threads are joined by a tree and at most 16 more terms, so the sum of squares is off by
     at most (32 + 5 + 16 + 1) u (its root by half of that); the sum x + residual, the mean,
     the added eps, the root, the reciprocal, two products, expf, its sum and a quotient
-    follow."""
-    return 27 * U + 14 * U
+    follow. For bf16 the gate's exponential is the SFU's, 2^(-gate log2 e): off by 4 u and, from
+    the rounding of its argument, 2 |gate| u, where |gate| stays below 10."""
+    return 27 * U + 14 * U + 24 * U
 
 
 def norm_grads(x, dy, weight=None, gate=None, dresidual=None, eps=1e-6):
@@ -111,9 +112,17 @@ def decay(g, sigmoid, lower_bound):
     return torch.exp(g), torch.ones_like(g)
 
 
+def decay_rel(g):
+    """What fp32 leaves of a and of 1 - a, relative: expf is off by 4 u; the SFU's exponential,
+    taken for bf16, by 4 u and 2 |g| u from the rounding of its argument g log2 e. A sum, a
+    quotient, the weighting of x and the product of a run's a follow (8 u)."""
+    return (12 + 2 * g.double().abs()) * U
+
+
 def scan(x, g, lens, s0=None, sigmoid=False, lower_bound=None):
     """(h [T, D], final states [N, D], bound on h's fp32 error, the same of the states)."""
     a, b = decay(g, sigmoid, lower_bound)
+    k = decay_rel(g)
     v = b * x.double()
     D = x.shape[1]
     hs, es, fins, fes = [], [], [], []
@@ -122,8 +131,7 @@ def scan(x, g, lens, s0=None, sigmoid=False, lower_bound=None):
         h = torch.zeros(D, dtype=torch.float64, device=x.device) if s0 is None else s0[n].double()
         m, e = h.abs(), torch.zeros_like(h)
         for t in range(at, at + T):
-            # a is off by 8 u (expf, sum, quotient, the product of a run's a), the weighted input by 9 u
-            e = a[t] * (e + 10 * U * m) + 10 * U * v[t].abs()
+            e = a[t] * (e + k[t] * m) + k[t] * v[t].abs()
             h = a[t] * h + v[t]
             m = a[t] * m + v[t].abs()
             e = e + 2 * U * m
@@ -140,6 +148,7 @@ def scan_grads(x, g, h, dout, lens, s0=None, dsT=None, sigmoid=False, lower_boun
     """(dx, dg, ds0) from the written-out derivative with h as given, and bounds on the fp32
     error of each."""
     a, b = decay(g, sigmoid, lower_bound)
+    r = decay_rel(g)
     T_, D = g.shape
     dx, dg, ex, eg = (torch.zeros(T_, D, dtype=torch.float64, device=g.device) for _ in range(4))
     d0, e0 = [], []
@@ -158,14 +167,14 @@ def scan_grads(x, g, h, dout, lens, s0=None, dsT=None, sigmoid=False, lower_boun
             k = hp - x[t].double() if sigmoid else hp
             km = hp.abs() + x[t].double().abs() if sigmoid else hp.abs()
             dx[t] = b[t] * d
-            ex[t] = b[t] * (e + 10 * U * m)
+            ex[t] = b[t] * (e + r[t] * m)
             dg[t] = d * a[t] * b[t] * k
-            eg[t] = a[t] * b[t] * km * (e + 24 * U * m)
+            eg[t] = a[t] * b[t] * km * (e + 2 * r[t] * m + 4 * U * m)
             if lower_bound is not None:
                 below = g[t].double() < lower_bound
                 dg[t][below] = 0
             c = a[t] * d
-            e = a[t] * (e + 10 * U * m)
+            e = a[t] * (e + r[t] * m)
             m = a[t] * m
         d0.append(c)
         e0.append(e)

@@ -145,9 +145,10 @@ def test_norm_rows_of_a_fused_projection_and_in_place_sum():
     fused = draw(4, 9, 700, dtype=torch.bfloat16, seed=1)
     for lo, D in ((0, 256), (8, 256), (1, 256), (3, 333), (130, 64)):
         x, g = fused[..., lo:lo + D], fused[..., lo + D:lo + 2 * D] if lo + 2 * D <= 700 else fused[..., :D]
-        assert torch.equal(kda.rms_norm(x, gate=g), kda.rms_norm(x.contiguous(), gate=g.contiguous()))
-        dx = kda.rms_norm_bwd(x, g)[0]
-        assert torch.equal(dx, kda.rms_norm_bwd(x.contiguous(), g.contiguous())[0])
+        want = ref.norm(x, gate=g)[0]
+        within("y", kda.rms_norm(x, gate=g), want, want.abs() * (half(x.dtype) + ref.norm_rel(D)))
+        rx, _, _, mag, _ = ref.norm_grads(x, g)
+        within("dx", kda.rms_norm_bwd(x, g)[0], rx, rx.abs() * half(x.dtype) + mag * (54 * U + 2 * ref.norm_rel(D)))
     x, res = draw(50, 640, dtype=torch.bfloat16, seed=2), draw(50, 640, dtype=torch.bfloat16, seed=3)
     y, s = kda.rms_norm(x, residual=res)
     for target in ("res", "x"):
