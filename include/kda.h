@@ -387,6 +387,9 @@ typedef struct {
     kda_dtype dtype;          /* of x, residual, gate, residual_out, and y without scales */
     kda_dtype weight_dtype;   /* F32, or dtype */
     long long rows;
+    int heads;                /* rows that lie back to back: [tokens, heads, D] activations have
+                               * rows = tokens * heads, and their strides are those between
+                               * tokens (at least heads * D). 0 or 1: strides between rows */
     int D;
     const void *x;
     long long x_stride;
@@ -417,7 +420,7 @@ typedef struct {
     kda_dtype dtype;          /* of x, dy, gate, dresidual, dx, dgate */
     kda_dtype weight_dtype;   /* of weight and dweight: F32, or dtype */
     long long rows;
-    int D;
+    int heads, D;             /* as kda_rms_norm_args */
     const void *x;
     long long x_stride;
     const void *dy;

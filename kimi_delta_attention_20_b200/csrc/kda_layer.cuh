@@ -6,9 +6,17 @@
 
 namespace kda {
 
+// Rows of a norm: `heads` rows of D channels back to back, `stride` between such groups
+// (heads 1: evenly spaced rows).
+struct NormRows {
+    const void *at;
+    long long stride;
+    int heads;
+};
+
 struct NormParams {
-    const void *x, *residual, *gate, *weight;
-    long long x_stride, residual_stride, gate_stride;
+    NormRows x, residual, gate;
+    const void *weight;
     int weight_f32;
     long long rows;
     int D;
@@ -21,8 +29,8 @@ struct NormParams {
 };
 
 struct NormBwdParams {
-    const void *x, *dy, *gate, *dresidual, *weight;
-    long long x_stride, dy_stride, gate_stride, dresidual_stride;
+    NormRows x, dy, gate, dresidual;
+    const void *weight;
     int weight_f32;
     long long rows;
     int D;

@@ -101,11 +101,19 @@ bool workspace_ok(const void *ws, size_t bytes, size_t need, size_t align) {
     return need == 0 || (ws && bytes >= need && reinterpret_cast<uintptr_t>(ws) % align == 0);
 }
 
-kda_status check_norm_shape(int dtype, int weight_dtype, long long rows, int D, float eps) {
+// The rows of a norm tensor; ones that follow one another are evenly spaced.
+kda::NormRows norm_rows(const void *at, long long token_stride, int heads, int D) {
+    if (token_stride == (long long)heads * D) return {at, D, 1};
+    return {at, token_stride, heads};
+}
+
+kda_status check_norm_shape(int dtype, int weight_dtype, long long rows, int heads, int D, float eps) {
     if (!dtype_ok(dtype) || (weight_dtype != KDA_DTYPE_F32 && weight_dtype != dtype)) return KDA_ERR_INVALID_ARGUMENT;
-    if (rows < 0 || D < 1 || !(eps >= 0.f)) return KDA_ERR_INVALID_ARGUMENT;
+    if (rows < 0 || heads < 0 || D < 1 || !(eps >= 0.f)) return KDA_ERR_INVALID_ARGUMENT;
     if (D > kMaxNormDim) return KDA_ERR_UNSUPPORTED;
     if (rows > (1LL << 40) / D) return KDA_ERR_INVALID_ARGUMENT;
+    // rows of several heads are numbered in 32 bits
+    if (heads > 1 && (rows % heads || rows > 0x7fffffffLL)) return KDA_ERR_INVALID_ARGUMENT;
     return KDA_OK;
 }
 
@@ -137,7 +145,7 @@ extern "C" {
 
 kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
     if (!a) return KDA_ERR_INVALID_ARGUMENT;
-    kda_status s = check_norm_shape(a->dtype, a->weight_dtype, a->rows, a->D, a->eps);
+    kda_status s = check_norm_shape(a->dtype, a->weight_dtype, a->rows, a->heads, a->D, a->eps);
     if (s != KDA_OK) return s;
     if (a->group_size != 0 && a->group_size != 32 && a->group_size != 64 && a->group_size != 128) return KDA_ERR_UNSUPPORTED;
     if (a->residual && a->gate) return KDA_ERR_UNSUPPORTED;
@@ -145,16 +153,18 @@ kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
     const size_t esz = size_of(a->dtype);
     kda::NormParams p{};
     Checker c;
-    p.x_stride = c.input(a->x, true, a->rows, a->D, a->x_stride, esz);
-    p.residual_stride = c.input(a->residual, false, a->rows, a->D, a->residual_stride, esz);
-    p.gate_stride = c.input(a->gate, false, a->rows, a->D, a->gate_stride, esz);
+    const int heads = a->heads > 1 ? a->heads : 1;
+    const long long tokens = a->rows / heads, width = (long long)heads * a->D;
+    p.x = norm_rows(a->x, c.input(a->x, true, tokens, width, a->x_stride, esz), heads, a->D);
+    p.residual = norm_rows(a->residual, c.input(a->residual, false, tokens, width, a->residual_stride, esz), heads, a->D);
+    p.gate = norm_rows(a->gate, c.input(a->gate, false, tokens, width, a->gate_stride, esz), heads, a->D);
     c.input(a->weight, false, 1, a->D, 0, size_of(a->weight_dtype));
     const int group = a->group_size ? a->group_size : a->D;
     c.output(a->y, true, a->rows, a->D, a->scales ? 1 : esz);
     c.output(a->scales, false, a->rows, (a->D + group - 1) / group, 4);
     // every thread reads its channels of a row before it writes them, so the sum may replace a term
-    const bool in_place = a->residual_out && ((a->residual_out == a->residual && p.residual_stride == a->D) ||
-                                              (a->residual_out == a->x && p.x_stride == a->D));
+    const bool in_place = a->residual_out && ((a->residual_out == a->residual && p.residual.stride == a->D) ||
+                                              (a->residual_out == a->x && p.x.stride == a->D));
     if (in_place) {
         for (int i = 0; i < c.nin; ++i)  // but no other input may lie there
             if (c.in[i].lo != reinterpret_cast<uintptr_t>(a->residual_out)) {
@@ -168,7 +178,7 @@ kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
         c.output(a->residual_out, false, a->rows, a->D, esz);
     }
     if (c.bad || !c.apart()) return KDA_ERR_INVALID_ARGUMENT;
-    p.x = a->x; p.residual = a->residual; p.gate = a->gate; p.weight = a->weight;
+    p.weight = a->weight;
     p.weight_f32 = a->weight_dtype == KDA_DTYPE_F32;
     p.rows = a->rows; p.D = a->D; p.eps = a->eps;
     p.y = a->y; p.residual_out = a->residual_out;
@@ -178,7 +188,7 @@ kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
 
 kda_status kda_rms_norm_bwd_workspace_size(const kda_rms_norm_bwd_args *a, size_t *bytes) {
     if (!a || !bytes) return KDA_ERR_INVALID_ARGUMENT;
-    kda_status s = check_norm_shape(a->dtype, a->weight_dtype, a->rows, a->D, a->eps);
+    kda_status s = check_norm_shape(a->dtype, a->weight_dtype, a->rows, a->heads, a->D, a->eps);
     if (s != KDA_OK) return s;
     *bytes = kda::rms_norm_bwd_workspace_bytes(a->rows, a->D, a->dtype == KDA_DTYPE_BF16, a->dweight != nullptr);
     return KDA_OK;
@@ -192,10 +202,12 @@ kda_status kda_rms_norm_bwd(const kda_rms_norm_bwd_args *a, void *stream) {
     const size_t esz = size_of(a->dtype), wsz = size_of(a->weight_dtype);
     kda::NormBwdParams p{};
     Checker c;
-    p.x_stride = c.input(a->x, a->rows > 0, a->rows, a->D, a->x_stride, esz);
-    p.dy_stride = c.input(a->dy, a->rows > 0, a->rows, a->D, a->dy_stride, esz);
-    p.gate_stride = c.input(a->gate, false, a->rows, a->D, a->gate_stride, esz);
-    p.dresidual_stride = c.input(a->dresidual, false, a->rows, a->D, a->dresidual_stride, esz);
+    const int heads = a->heads > 1 ? a->heads : 1;
+    const long long tokens = a->rows / heads, width = (long long)heads * a->D;
+    p.x = norm_rows(a->x, c.input(a->x, a->rows > 0, tokens, width, a->x_stride, esz), heads, a->D);
+    p.dy = norm_rows(a->dy, c.input(a->dy, a->rows > 0, tokens, width, a->dy_stride, esz), heads, a->D);
+    p.gate = norm_rows(a->gate, c.input(a->gate, false, tokens, width, a->gate_stride, esz), heads, a->D);
+    p.dresidual = norm_rows(a->dresidual, c.input(a->dresidual, false, tokens, width, a->dresidual_stride, esz), heads, a->D);
     c.input(a->weight, false, 1, a->D, 0, wsz);
     c.output(a->dx, a->rows > 0, a->rows, a->D, esz);
     c.output(a->dgate, a->rows > 0 && a->gate, a->rows, a->D, esz);
@@ -206,7 +218,7 @@ kda_status kda_rms_norm_bwd(const kda_rms_norm_bwd_args *a, void *stream) {
         return launched(cudaMemsetAsync(a->dweight, 0, (size_t)a->D * wsz, static_cast<cudaStream_t>(stream)));
     }
     if (!workspace_ok(a->workspace, a->workspace_bytes, need, 16)) return KDA_ERR_WORKSPACE;
-    p.x = a->x; p.dy = a->dy; p.gate = a->gate; p.dresidual = a->dresidual; p.weight = a->weight;
+    p.weight = a->weight;
     p.weight_f32 = a->weight_dtype == KDA_DTYPE_F32;
     p.rows = a->rows; p.D = a->D; p.eps = a->eps;
     p.dx = a->dx; p.dgate = a->dgate; p.dweight = a->dweight;

@@ -149,9 +149,14 @@ __device__ __forceinline__ float group_scale(float top, int pow2) {
 
 // A row's accesses of a thread, as stored; zeros without the row.
 template <typename T, int G, int TPR, int NA>
-__device__ __forceinline__ void fetch_row(const void *base, long long stride, long long row, bool ok, int t, int D, Bits<G> (&q)[NA]) {
+__device__ __forceinline__ void fetch_row(const NormRows &rows, long long row, bool ok, int t, int D, Bits<G> (&q)[NA]) {
     constexpr int P = access_channels<T, G>();
-    const T *r = static_cast<const T *>(base) + row * stride;
+    long long at = row * rows.stride;
+    if (rows.heads > 1) {  // 32-bit row numbers, see the entry points
+        const unsigned token = (unsigned)row / (unsigned)rows.heads;
+        at = token * rows.stride + (long long)((unsigned)row - token * rows.heads) * D;
+    }
+    const T *r = static_cast<const T *>(rows.at) + at;
 #pragma unroll
     for (int i = 0; i < NA; ++i) q[i] = fetch<T, G>(r, (i * TPR + t) * P, ok && (i * TPR + t) * P < D);
 }
@@ -195,9 +200,7 @@ inline int norm_ctas(long long rows, NormShape s, bool backward) {
 inline RowAccess norm_access(const NormParams &p, bool bf16) {
     const size_t esz = bf16 ? 2 : 4;
     RowAccess ac;
-    ac.rows(p.x, p.x_stride, p.D, esz);
-    ac.rows(p.residual, p.residual_stride, p.D, esz);
-    ac.rows(p.gate, p.gate_stride, p.D, esz);
+    for (const NormRows *r : {&p.x, &p.residual, &p.gate}) ac.rows(r->at, r->stride, p.D, esz);
     ac.rows(p.weight, p.D, p.D, p.weight_f32 ? 4 : esz);
     ac.rows(p.residual_out, p.D, p.D, esz);
     return ac;

@@ -22,14 +22,13 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), norm_resident(true, TPR, 
     const long long step = (long long)gridDim.x * ROWS;
     long long row = (long long)blockIdx.x * ROWS + lr;
     // the third tensor: the gate, or the cotangent of the sum
-    const void *third = GATE ? p.gate : p.dresidual;
-    const long long third_stride = GATE ? p.gate_stride : p.dresidual_stride;
+    const NormRows &third = GATE ? p.gate : p.dresidual;
     Bits<G> bx[NA], bd[NA], bt[NA];
     auto fetch_all = [&](long long r) {
         const bool ok = r < p.rows;
-        fetch_row<T, G, TPR, NA>(p.x, p.x_stride, r, ok, t, D, bx);
-        fetch_row<T, G, TPR, NA>(p.dy, p.dy_stride, r, ok, t, D, bd);
-        fetch_row<T, G, TPR, NA>(third, third_stride, r, ok && third, t, D, bt);
+        fetch_row<T, G, TPR, NA>(p.x, r, ok, t, D, bx);
+        fetch_row<T, G, TPR, NA>(p.dy, r, ok, t, D, bd);
+        fetch_row<T, G, TPR, NA>(third, r, ok && third.at, t, D, bt);
     };
     fetch_all(row);
     int flip = 0;  // two buffers in turn: one barrier a row
@@ -112,7 +111,7 @@ template <typename T, int G, int TPR, int NU> struct Bwd {
     static cudaError_t run(const NormBwdParams &p, cudaStream_t st) {
         const int ctas = norm_ctas(p.rows, {TPR, NU}, true);
         count_launch();
-        if (p.gate) norm_bwd_kernel<T, G, TPR, NU, true><<<ctas, norm_threads<TPR>(), 0, st>>>(p);
+        if (p.gate.at) norm_bwd_kernel<T, G, TPR, NU, true><<<ctas, norm_threads<TPR>(), 0, st>>>(p);
         else norm_bwd_kernel<T, G, TPR, NU, false><<<ctas, norm_threads<TPR>(), 0, st>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || !p.dweight) return e;
@@ -131,10 +130,7 @@ size_t rms_norm_bwd_workspace_bytes(long long rows, int D, bool, bool weight) {
 cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, bool bf16, cudaStream_t st) {
     const size_t esz = bf16 ? 2 : 4, wsz = p.weight_f32 ? 4 : esz;
     RowAccess ac;
-    ac.rows(p.x, p.x_stride, p.D, esz);
-    ac.rows(p.dy, p.dy_stride, p.D, esz);
-    ac.rows(p.gate, p.gate_stride, p.D, esz);
-    ac.rows(p.dresidual, p.dresidual_stride, p.D, esz);
+    for (const NormRows *r : {&p.x, &p.dy, &p.gate, &p.dresidual}) ac.rows(r->at, r->stride, p.D, esz);
     ac.rows(p.weight, p.D, p.D, wsz);
     ac.rows(p.dx, p.D, p.D, esz);
     ac.rows(p.dgate, p.D, p.D, esz);

@@ -12,7 +12,7 @@ template <typename T, int G, int TPR, int NU> struct Fwd {
         return cudaGetLastError();
     }
     static cudaError_t run(const NormParams &p, cudaStream_t st) {
-        return p.residual ? launch<kResidual>(p, st) : p.gate ? launch<kGate>(p, st) : launch<kPlain>(p, st);
+        return p.residual.at ? launch<kResidual>(p, st) : p.gate.at ? launch<kGate>(p, st) : launch<kPlain>(p, st);
     }
 };
 

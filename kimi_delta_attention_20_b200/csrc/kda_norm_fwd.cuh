@@ -17,12 +17,12 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), norm_resident(false, TPR,
     __shared__ float red[2][2][1][norm_red<TPR>()];
     const int t = threadIdx.x % TPR, lr = threadIdx.x / TPR, D = p.D;
     const float per = 1.f / D;
-    const void *other = MODE == kResidual ? p.residual : p.gate;
-    const long long other_stride = MODE == kResidual ? p.residual_stride : p.gate_stride, step = (long long)gridDim.x * ROWS;
+    const NormRows &other = MODE == kResidual ? p.residual : p.gate;
+    const long long step = (long long)gridDim.x * ROWS;
     long long row = (long long)blockIdx.x * ROWS + lr;
     Bits<G> bx[NA], bo[NA];
-    fetch_row<T, G, TPR, NA>(p.x, p.x_stride, row, row < p.rows, t, D, bx);
-    if (MODE != kPlain) fetch_row<T, G, TPR, NA>(other, other_stride, row, row < p.rows, t, D, bo);
+    fetch_row<T, G, TPR, NA>(p.x, row, row < p.rows, t, D, bx);
+    if (MODE != kPlain) fetch_row<T, G, TPR, NA>(other, row, row < p.rows, t, D, bo);
     int flip = 0;  // two buffers in turn: one barrier a reduction
     for (long long base = row - lr; base < p.rows; base += step, row += step, flip ^= 1) {
         const bool ok = row < p.rows;  // threads without a row take part in the reductions
@@ -33,8 +33,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), norm_resident(false, TPR,
             widen<T, G>(bx[q], s + q * P);
             cur[q] = bo[q];
         }
-        fetch_row<T, G, TPR, NA>(p.x, p.x_stride, row + step, row + step < p.rows, t, D, bx);
-        if (MODE != kPlain) fetch_row<T, G, TPR, NA>(other, other_stride, row + step, row + step < p.rows, t, D, bo);
+        fetch_row<T, G, TPR, NA>(p.x, row + step, row + step < p.rows, t, D, bx);
+        if (MODE != kPlain) fetch_row<T, G, TPR, NA>(other, row + step, row + step < p.rows, t, D, bo);
         if (MODE == kResidual)
 #pragma unroll
             for (int q = 0; q < NA; ++q) {

@@ -9,7 +9,6 @@ requires grad (the 8-bit norm and the single-token forms have none).
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional, Tuple
 
 import torch
@@ -18,24 +17,30 @@ from torch.autograd.function import once_differentiable
 from . import _abi
 from .ops import _DTYPES, _seqlens
 
-_byref = ctypes.byref
+_F32 = _abi.KDA_DTYPE_F32
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device; what torch.cuda.current_stream wraps
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _dev(name, t):
+    """Device index of a CUDA tensor."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-def _need(name, t, device=None):
+def _same_dev(name, t, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
 
 
 def _dtype(name, t):
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be float32 or bfloat16")
-    return _DTYPES[t.dtype]
+    return code
 
 
 def _row_stride(t: torch.Tensor):
@@ -61,70 +66,81 @@ def _row_stride(t: torch.Tensor):
     return step if step >= shape[-1] else None
 
 
-def _act(name, t, like, shape=None):
-    """Row stride of an activation with the dtype and device of ``like``."""
-    _need(name, t, like.device)
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} must have dtype {like.dtype}")
-    if t.shape != (like.shape if shape is None else shape):
-        raise ValueError(f"{name} must have shape {tuple(like.shape if shape is None else shape)}")
-    stride = _row_stride(t)
+def _act(name, t, like, dev):
+    """(pointer, row stride) of an activation with the dtype, shape and device of ``like``."""
+    if t is not like:
+        _same_dev(name, t, dev)
+        if t.dtype != like.dtype:
+            raise ValueError(f"{name} must have dtype {like.dtype}")
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    stride = 0 if t.is_contiguous() else _row_stride(t)
     if stride is None:
         raise ValueError(f"{name} must have contiguous channels and evenly spaced rows")
-    return stride
+    return t.data_ptr(), stride
 
 
-def _cotangent(name, t, like, shape=None):
+def _cotangent(name, t, like, dev):
     """A cotangent as autograd hands it over: any strides, brought to dense rows if need be."""
-    _need(name, t, like.device)
-    t = t.to(like.dtype)
+    _same_dev(name, t, dev)
+    if t.dtype != like.dtype:
+        t = t.to(like.dtype)
     return t if _row_stride(t) is not None else t.contiguous()
 
 
-def _state(name, t, shape, device):
-    """Pointer of a dense fp32 tensor, or None."""
+def _state(name, t, shape, dev):
+    """Pointer of a dense fp32 tensor, 0 for none."""
     if t is None:
-        return None
-    _need(name, t, device)
+        return 0
+    _same_dev(name, t, dev)
     if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
-def _out(name, t, shape, dtype, device):
-    """The output buffer: the caller's, checked, or a new one."""
+def _out(name, t, like, dev):
+    """The output buffer of activations: the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return _out_as(name, t, like.shape, like.dtype, like.device, dev)
+
+
+def _out_as(name, t, shape, dtype, device, dev):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(name, t, device)
+    _same_dev(name, t, dev)
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t
 
 
-def _launch(fn, a, device, what):
-    if device.index == torch.cuda.current_device():
-        status = fn(_byref(a), torch.cuda.current_stream(device).cuda_stream)
+def _ptr(t: Optional[torch.Tensor]):
+    return 0 if t is None else t.data_ptr()
+
+
+def _launch(call, packed, dev):
+    """Queues a call on the current stream of its device."""
+    if dev == torch.cuda.current_device():
+        status = call.fn(packed, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            status = fn(_byref(a), torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(dev):
+            status = call.fn(packed, _raw_stream(dev))
     if status:
-        _abi.check(status, what)
+        _abi.check(status, call.name)
 
 
-def _scratch(size_fn, a, workspace, device, what):
-    """Gives the call its workspace: the caller's, or a new one where one is needed."""
-    n = ctypes.c_size_t(0)
-    _abi.check(size_fn(_byref(a), _byref(n)), what)
-    if not n.value:
-        return None
-    if workspace is None:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=device)
-    else:
-        _need("workspace", workspace, device)
+def _launch_scratch(call, fields, workspace, device, dev):
+    """As _launch of the packed ``fields``, followed by the workspace that the call needs: the
+    caller's, or a new one."""
+    need = call.size(call.pack(*fields, 0, 0))
+    if workspace is not None:
+        _same_dev("workspace", workspace, dev)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    return workspace  # kept alive by the caller until the launch
+        need = workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _launch(call, call.pack(*fields, _ptr(workspace), need), dev)
 
 
 def _span(x, cu_seqlens, cu_seqlens_cpu, features):
@@ -149,10 +165,6 @@ def _span(x, cu_seqlens, cu_seqlens_cpu, features):
     return B, T, cu_seqlens.numel() - 1, dev, host
 
 
-def _wants_grad(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-
-
 def _no_outs(**outs):
     for name, t in outs.items():
         if t is not None:
@@ -161,48 +173,83 @@ def _no_outs(**outs):
 
 # --------------------------------------------------------------------------- RMS norm
 
-def _weight(weight, x):
+def _weight(weight, x, dev):
     """(pointer, dtype code) of a norm weight."""
     if weight is None:
-        return None, _abi.KDA_DTYPE_F32
-    _need("weight", weight, x.device)
+        return 0, _F32
+    _same_dev("weight", weight, dev)
     if weight.shape != x.shape[-1:] or weight.dtype not in (torch.float32, x.dtype) or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous tensor of {x.shape[-1]} float32 or {x.dtype} values")
     return weight.data_ptr(), _DTYPES[weight.dtype]
 
 
-def _norm_args(x, weight, residual, gate, eps, residual_out):
-    _need("x", x)
+def _norm_rows(tensors, like, dev):
+    """(heads, [(pointer, stride) of each tensor or (0, 0)]): rows evenly spaced, or [.., heads, D]
+    whose heads lie back to back and whose tokens are evenly spaced -- a slice of a fused projection."""
+    rows, even = [], True
+    for name, t in tensors:
+        if t is None:
+            rows.append((0, 0))
+            continue
+        if t is not like:
+            _same_dev(name, t, dev)
+            if t.dtype != like.dtype:
+                raise ValueError(f"{name} must have dtype {like.dtype}")
+            if t.shape != like.shape:
+                raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+        stride = 0 if t.is_contiguous() else _row_stride(t)
+        even = even and stride is not None
+        rows.append((t.data_ptr(), stride))
+    if even:
+        return 1, rows
+    H, D = like.shape[-2:] if like.dim() > 1 else (1, like.shape[-1])
+    for i, (name, t) in enumerate(tensors):
+        if t is None:
+            continue
+        dense = (D == 1 or t.stride(-1) == 1) and (H == 1 or t.stride(-2) == D)
+        stride = _row_stride(t.flatten(-2)) if t.dim() > 1 and dense else None
+        if stride is None:
+            raise ValueError(f"{name} must have contiguous channels and evenly spaced rows (or heads back to back in evenly spaced tokens)")
+        rows[i] = (t.data_ptr(), stride)
+    return H, rows
+
+
+def _norm(x, weight, residual, gate, eps, residual_out, quant=None, out=None):
+    """One forward call; quant: (group_size, pow2_scales, scales_out) for the 8-bit output.
+    Returns (y, scales or None, s or None)."""
+    call = _abi.call("kda_rms_norm")
+    dev = _dev("x", x)
     dt = _dtype("x", x)
     if x.dim() < 1:
         raise ValueError("x must be [..., D]")
     D = x.shape[-1]
-    rows = x.numel() // D if D else 0
-    stride = _act("x", x, x)
-    a = _abi.RMSNormArgs(dtype=dt, rows=rows, D=D, x=_ptr(x), x_stride=stride, eps=eps)
-    a.weight, a.weight_dtype = _weight(weight, x)
-    if residual is not None and gate is not None:
-        raise ValueError("residual and gate cannot be combined")
+    wp, wdt = _weight(weight, x, dev)
+    heads, ((xp, xs), (rp, rs), (gp, gs)) = _norm_rows((("x", x), ("residual", residual), ("gate", gate)), x, dev)
     if residual is not None:
-        a.residual_stride = _act("residual", residual, x)
-        a.residual = _ptr(residual)
-        residual_out = _out("residual_out", residual_out, x.shape, x.dtype, x.device)
-        a.residual_out = _ptr(residual_out)
+        if gate is not None:
+            raise ValueError("residual and gate cannot be combined")
+        residual_out = _out("residual_out", residual_out, x, dev)
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
-    if gate is not None:
-        a.gate_stride = _act("gate", gate, x)
-        a.gate = _ptr(gate)
-    return a, residual_out
+    group = pow2 = 0
+    scales = None
+    if quant is None:
+        y = _out("out", out, x, dev)
+    else:
+        group, pow2, scales = quant
+        if group not in (0, 32, 64, 128):
+            raise ValueError("group_size must be 0 (the whole row), 32, 64 or 128")
+        y = _out_as("out", out, x.shape, torch.float8_e4m3fn, x.device, dev)
+        shape = (*x.shape[:-1], -(-D // group) if group else 1)
+        scales = _out_as("scales_out", scales, shape, torch.float32, x.device, dev)
+    _launch(call, call.pack(dt, wdt, x.numel() // D if D else 0, heads, D, xp, xs, rp, rs, gp, gs, wp, eps, y.data_ptr(),
+                            _ptr(residual_out), _ptr(scales), group, int(pow2)), dev)
+    return y, scales, residual_out
 
 
 def _rms_norm_fwd(x, weight, residual, gate, eps, out=None, residual_out=None):
-    lib = _abi.load()
-    a, residual_out = _norm_args(x, weight, residual, gate, eps, residual_out)
-    y = _out("out", out, x.shape, x.dtype, x.device)
-    a.y = _ptr(y)
-    _launch(lib.kda_rms_norm, a, x.device, "kda_rms_norm")
-    return y if residual is None else (y, residual_out)
+    y, _, s = _norm(x, weight, residual, gate, eps, residual_out, out=out)
+    return y if residual is None else (y, s)
 
 
 class _RMSNorm(torch.autograd.Function):
@@ -237,7 +284,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual
     sum, s is the sum in x's dtype (written to ``residual_out`` if given, which may be
     ``residual`` or ``x`` itself). Gradients flow to x, weight, residual and gate.
     """
-    if _wants_grad(x, weight, residual, gate):
+    if torch.is_grad_enabled() and (x.requires_grad or any(t is not None and t.requires_grad for t in (weight, residual, gate))):
         _no_outs(out=out, residual_out=residual_out)
         return _RMSNorm.apply(x, weight, residual, gate, eps)
     return _rms_norm_fwd(x, weight, residual, gate, eps, out, residual_out)
@@ -253,19 +300,10 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, re
     the scale max(max|y| / 448, 2^-100), with ``pow2_scales`` rounded up to a power of two.
     No gradients: inputs that require grad are refused.
     """
-    if _wants_grad(x, weight, residual, gate):
+    if torch.is_grad_enabled() and (x.requires_grad or any(t is not None and t.requires_grad for t in (weight, residual, gate))):
         raise NotImplementedError("rms_norm_quant has no gradients; use rms_norm")
-    lib = _abi.load()
-    a, residual_out = _norm_args(x, weight, residual, gate, eps, residual_out)
-    if group_size not in (0, 32, 64, 128):
-        raise ValueError("group_size must be 0 (the whole row), 32, 64 or 128")
-    D = x.shape[-1]
-    groups = -(-D // group_size) if group_size else 1
-    q = _out("out", out, x.shape, torch.float8_e4m3fn, x.device)
-    scales = _out("scales_out", scales_out, (*x.shape[:-1], groups), torch.float32, x.device)
-    a.y, a.scales, a.group_size, a.pow2_scales = _ptr(q), _ptr(scales), group_size, int(pow2_scales)
-    _launch(lib.kda_rms_norm, a, x.device, "kda_rms_norm")
-    return (q, scales) if residual is None else (q, scales, residual_out)
+    q, scales, s = _norm(x, weight, residual, gate, eps, residual_out, (group_size, pow2_scales, scales_out), out)
+    return (q, scales) if residual is None else (q, scales, s)
 
 
 def rms_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
@@ -275,57 +313,49 @@ def rms_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.Tenso
     of y. x is what was normed: with a residual, the sum s that the forward returned; dx is
     then the gradient of both terms, and ``dresidual``, the cotangent of s, is added to it.
     """
-    lib = _abi.load()
-    _need("x", x)
+    call = _abi.call("kda_rms_norm_bwd")
+    dev = _dev("x", x)
     dt = _dtype("x", x)
-    dy = _cotangent("dy", dy, x)
     D = x.shape[-1]
-    a = _abi.RMSNormBwdArgs(dtype=dt, rows=x.numel() // D if D else 0, D=D, x_stride=_act("x", x, x), x=_ptr(x),
-                            dy_stride=_act("dy", dy, x), dy=_ptr(dy), eps=eps)
-    a.weight, a.weight_dtype = _weight(weight, x)
-    dgate = dw = None
+    wp, wdt = _weight(weight, x, dev)
     if gate is not None and dresidual is not None:
         raise ValueError("dresidual and gate cannot be combined")
-    if gate is not None:
-        a.gate_stride = _act("gate", gate, x)
-        a.gate = _ptr(gate)
-        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        a.dgate = _ptr(dgate)
+    # cotangents come with any strides; dense ones go with every layout of x and gate
+    dy = _cotangent("dy", dy, x, dev)
     if dresidual is not None:
-        dresidual = _cotangent("dresidual", dresidual, x)
-        a.dresidual_stride = _act("dresidual", dresidual, x)
-        a.dresidual = _ptr(dresidual)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.dx = _ptr(dx)
+        dresidual = _cotangent("dresidual", dresidual, x, dev)
+    heads, ((xp, xs), (dp, ds), (gp, gs), (rp, rs)) = _norm_rows((("x", x), ("dy", dy), ("gate", gate), ("dresidual", dresidual)), x, dev)
+    dgate = dw = None
+    if gate is not None:
+        dgate = _out("dgate", None, x, dev)
+    dx = _out("dx", None, x, dev)
     if weight is not None and want_dweight:
         dw = torch.empty_like(weight)
-        a.dweight = _ptr(dw)
-    ws = _scratch(lib.kda_rms_norm_bwd_workspace_size, a, workspace, x.device, "kda_rms_norm_bwd_workspace_size")  # noqa: F841
-    _launch(lib.kda_rms_norm_bwd, a, x.device, "kda_rms_norm_bwd")
+    _launch_scratch(call, (dt, wdt, x.numel() // D if D else 0, heads, D, xp, xs, dp, ds, gp, gs, rp, rs, wp, eps, dx.data_ptr(),
+                           _ptr(dgate), _ptr(dw)), workspace, x.device, dev)
     return dx, dgate, dw
 
 
 # --------------------------------------------------------------------------- causal convolution
 
-def _conv_weight(conv_w, x):
-    _need("conv_w", conv_w, x.device)
+def _conv_weight(conv_w, x, dev):
+    _same_dev("conv_w", conv_w, dev)
     if conv_w.dtype != torch.float32 or conv_w.dim() != 2 or conv_w.shape[0] != x.shape[-1] or not conv_w.is_contiguous():
         raise ValueError(f"conv_w must be a contiguous float32 tensor [{x.shape[-1]}, K]")
     return conv_w.shape[1]
 
 
 def _causal_conv_fwd(x, conv_w, initial_state, want_final, cu_seqlens, cu_seqlens_cpu, out=None, final_state_out=None):
-    lib = _abi.load()
-    _need("x", x)
+    call = _abi.call("kda_causal_conv")
+    dev = _dev("x", x)
     dt = _dtype("x", x)
     B, T, N, cu, cu_host = _span(x, cu_seqlens, cu_seqlens_cpu, "C")
-    C, K = x.shape[2], _conv_weight(conv_w, x)
-    stride = _act("x", x, x)
-    s0 = _state("initial_state", initial_state, (N, C, K), x.device)
-    y = _out("out", out, x.shape, x.dtype, x.device)
-    fs = _out("final_state_out", final_state_out, (N, C, K), torch.float32, x.device) if want_final else None
-    a = _abi.ConvArgs(dt, B, T, C, K, _ptr(x), stride, conv_w.data_ptr(), s0, _ptr(fs), _ptr(y), _ptr(cu), _ptr(cu_host), N)
-    _launch(lib.kda_causal_conv, a, x.device, "kda_causal_conv")
+    C, K = x.shape[2], _conv_weight(conv_w, x, dev)
+    xp, xs = _act("x", x, x, dev)
+    s0 = _state("initial_state", initial_state, (N, C, K), dev)
+    y = _out("out", out, x, dev)
+    fs = _out_as("final_state_out", final_state_out, (N, C, K), torch.float32, x.device, dev) if want_final else None
+    _launch(call, call.pack(dt, B, T, C, K, xp, xs, conv_w.data_ptr(), s0, _ptr(fs), y.data_ptr(), _ptr(cu), _ptr(cu_host), N), dev)
     return y, fs, cu, cu_host
 
 
@@ -365,7 +395,7 @@ def causal_conv(x: torch.Tensor, conv_w: torch.Tensor, *, initial_state: Optiona
     ``decode_token`` and ``causal_conv_step`` continue from the windows. Gradients flow to x,
     conv_w and initial_state.
     """
-    if _wants_grad(x, conv_w, initial_state):
+    if torch.is_grad_enabled() and (x.requires_grad or conv_w.requires_grad or (initial_state is not None and initial_state.requires_grad)):
         _no_outs(out=out, final_state_out=final_state_out)
         return _CausalConv.apply(x, conv_w, initial_state, output_final_state, cu_seqlens, cu_seqlens_cpu)
     return _causal_conv_fwd(x, conv_w, initial_state, output_final_state, cu_seqlens, cu_seqlens_cpu, out, final_state_out)[:2]
@@ -376,18 +406,19 @@ def causal_conv_step(x: torch.Tensor, conv_w: torch.Tensor, conv_state: torch.Te
     """One token of N sequences: x [N, C], conv_w [C, K] float32, conv_state [N, C, K] float32,
     updated IN PLACE (shifted one slot, x last). Returns silu(w . window) [N, C].
     """
-    lib = _abi.load()
-    _need("x", x)
+    call = _abi.call("kda_causal_conv_step")
+    dev = _dev("x", x)
     dt = _dtype("x", x)
     if x.dim() != 2:
         raise ValueError("x must be [N, C]")
     N, C = x.shape
-    K = _conv_weight(conv_w, x)
-    stride = _act("x", x, x)
-    s = _state("conv_state", conv_state, (N, C, K), x.device)
-    y = _out("out", out, x.shape, x.dtype, x.device)
-    a = _abi.ConvStepArgs(dt, N, C, K, _ptr(x), stride, conv_w.data_ptr(), s, _ptr(y))
-    _launch(lib.kda_causal_conv_step, a, x.device, "kda_causal_conv_step")
+    K = _conv_weight(conv_w, x, dev)
+    xp, xs = _act("x", x, x, dev)
+    if conv_state is None:
+        raise ValueError("conv_state is required")
+    s = _state("conv_state", conv_state, (N, C, K), dev)
+    y = _out("out", out, x, dev)
+    _launch(call, call.pack(dt, N, C, K, xp, xs, conv_w.data_ptr(), s, y.data_ptr()), dev)
     return y
 
 
@@ -400,25 +431,25 @@ def causal_conv_bwd(x: torch.Tensor, conv_w: torch.Tensor, dy: torch.Tensor, *,
     cotangents ``dy`` of y and, optionally, ``dfinal_state`` [N, C, K] float32 of the final
     windows. dinitial_state comes with an initial_state unless asked for otherwise.
     """
-    lib = _abi.load()
-    _need("x", x)
+    call = _abi.call("kda_causal_conv_bwd")
+    dev = _dev("x", x)
     dt = _dtype("x", x)
     B, T, N, cu, cu_host = _span(x, cu_seqlens, cu_seqlens_cpu, "C")
-    C, K = x.shape[2], _conv_weight(conv_w, x)
-    dy = _cotangent("dy", dy, x)
+    C, K = x.shape[2], _conv_weight(conv_w, x, dev)
+    xp, xs = _act("x", x, x, dev)
+    dy = _cotangent("dy", dy, x, dev)
+    dp, dst = _act("dy", dy, x, dev)
+    s0 = _state("initial_state", initial_state, (N, C, K), dev)
     if dfinal_state is not None:
         dfinal_state = dfinal_state.contiguous()
+    dsT = _state("dfinal_state", dfinal_state, (N, C, K), dev)
     if want_dinitial_state is None:
         want_dinitial_state = initial_state is not None
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dx = _out("dx", None, x, dev)
     dw = torch.empty_like(conv_w) if want_dconv_w else None
     ds0 = torch.empty((N, C, K), dtype=torch.float32, device=x.device) if want_dinitial_state else None
-    a = _abi.ConvBwdArgs(dt, B, T, C, K, _ptr(x), _act("x", x, x), _ptr(dy), _act("dy", dy, x), conv_w.data_ptr(),
-                         _state("initial_state", initial_state, (N, C, K), x.device),
-                         _state("dfinal_state", dfinal_state, (N, C, K), x.device), _ptr(dx), _ptr(dw), _ptr(ds0),
-                         _ptr(cu), _ptr(cu_host), N)
-    ws = _scratch(lib.kda_causal_conv_bwd_workspace_size, a, workspace, x.device, "kda_causal_conv_bwd_workspace_size")  # noqa: F841
-    _launch(lib.kda_causal_conv_bwd, a, x.device, "kda_causal_conv_bwd")
+    _launch_scratch(call, (dt, B, T, C, K, xp, xs, dp, dst, conv_w.data_ptr(), s0, dsT, dx.data_ptr(), _ptr(dw), _ptr(ds0), _ptr(cu),
+                           _ptr(cu_host), N), workspace, x.device, dev)
     return dx, dw, ds0
 
 
@@ -437,20 +468,19 @@ def _scan_gate(sigmoid, lower_bound):
 
 def _gated_scan_fwd(x, g, initial_state, want_final, sigmoid, lower_bound, cu_seqlens, cu_seqlens_cpu, out=None,
                     final_state_out=None, workspace=None):
-    lib = _abi.load()
-    _need("x", x)
+    call = _abi.call("kda_gated_scan")
+    dev = _dev("x", x)
     dt = _dtype("x", x)
     gate, has_lb, lb = _scan_gate(sigmoid, lower_bound)
     B, T, N, cu, cu_host = _span(x, cu_seqlens, cu_seqlens_cpu, "D")
     D = x.shape[2]
-    xs, gs = _act("x", x, x), _act("g", g, x)
-    s0 = _state("initial_state", initial_state, (N, D), x.device)
-    h = _out("out", out, x.shape, x.dtype, x.device)
-    fs = _out("final_state_out", final_state_out, (N, D), torch.float32, x.device) if want_final else None
-    a = _abi.ScanArgs(dt, gate, B, T, D, _ptr(x), xs, _ptr(g), gs, _ptr(h), s0, _ptr(fs), _ptr(cu), _ptr(cu_host), N,
-                      has_lb, lb)
-    ws = _scratch(lib.kda_gated_scan_workspace_size, a, workspace, x.device, "kda_gated_scan_workspace_size")  # noqa: F841
-    _launch(lib.kda_gated_scan, a, x.device, "kda_gated_scan")
+    xp, xs = _act("x", x, x, dev)
+    gp, gs = _act("g", g, x, dev)
+    s0 = _state("initial_state", initial_state, (N, D), dev)
+    h = _out("out", out, x, dev)
+    fs = _out_as("final_state_out", final_state_out, (N, D), torch.float32, x.device, dev) if want_final else None
+    _launch_scratch(call, (dt, gate, B, T, D, xp, xs, gp, gs, h.data_ptr(), s0, _ptr(fs), _ptr(cu), _ptr(cu_host), N, has_lb, lb),
+                    workspace, x.device, dev)
     return h, fs, cu, cu_host
 
 
@@ -493,7 +523,7 @@ def chunk_gated_scan(x: torch.Tensor, g: torch.Tensor, *, initial_state: Optiona
     Gradients flow to x, g and initial_state. A ``workspace`` passed in belongs to one call at
     a time (captured graphs that may overlap need one each).
     """
-    if _wants_grad(x, g, initial_state):
+    if torch.is_grad_enabled() and (x.requires_grad or g.requires_grad or (initial_state is not None and initial_state.requires_grad)):
         _no_outs(out=out, final_state_out=final_state_out, workspace=workspace)
         return _GatedScan.apply(x, g, initial_state, output_final_state, use_gate_sigmoid_in_kernel, lower_bound,
                                 cu_seqlens, cu_seqlens_cpu)
@@ -508,17 +538,20 @@ def gated_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *, us
     read when ``state_out`` (a second buffer, disjoint from it) receives the new state. Gate
     arguments as in ``chunk_gated_scan``. Returns h [N, D].
     """
-    lib = _abi.load()
-    _need("x", x)
+    call = _abi.call("kda_gated_scan_step")
+    dev = _dev("x", x)
     dt = _dtype("x", x)
     gate, has_lb, lb = _scan_gate(use_gate_sigmoid_in_kernel, lower_bound)
     if x.dim() != 2:
         raise ValueError("x must be [N, D]")
-    xs, gs = _act("x", x, x), _act("g", g, x)
-    s, so = _state("state", state, x.shape, x.device), _state("state_out", state_out, x.shape, x.device)
-    h = _out("out", out, x.shape, x.dtype, x.device)
-    a = _abi.ScanStepArgs(dt, gate, x.shape[0], x.shape[1], _ptr(x), xs, _ptr(g), gs, s, so, _ptr(h), has_lb, lb)
-    _launch(lib.kda_gated_scan_step, a, x.device, "kda_gated_scan_step")
+    N, D = x.shape
+    xp, xs = _act("x", x, x, dev)
+    gp, gs = _act("g", g, x, dev)
+    if state is None:
+        raise ValueError("state is required")
+    s, so = _state("state", state, (N, D), dev), _state("state_out", state_out, (N, D), dev)
+    h = _out("out", out, x, dev)
+    _launch(call, call.pack(dt, gate, N, D, xp, xs, gp, gs, s, so, h.data_ptr(), has_lb, lb), dev)
     return h
 
 
@@ -533,28 +566,27 @@ def chunk_gated_scan_bwd(x: Optional[torch.Tensor], g: torch.Tensor, h: torch.Te
     the lower bound is taken (g < lower_bound). dinitial_state comes with an initial_state
     unless asked for otherwise.
     """
-    lib = _abi.load()
-    _need("g", g)
+    call = _abi.call("kda_gated_scan_bwd")
+    dev = _dev("g", g)
     dt = _dtype("g", g)
     gate, has_lb, lb = _scan_gate(use_gate_sigmoid_in_kernel, lower_bound)
     if use_gate_sigmoid_in_kernel and x is None:
         raise ValueError("x is required with use_gate_sigmoid_in_kernel")
-    if not use_gate_sigmoid_in_kernel:
-        x = None
     B, T, N, cu, cu_host = _span(g, cu_seqlens, cu_seqlens_cpu, "D")
     D = g.shape[2]
-    dout = _cotangent("dout", dout, g)
+    xp, xs = _act("x", x, g, dev) if use_gate_sigmoid_in_kernel else (0, 0)
+    gp, gs = _act("g", g, g, dev)
+    hp, hs = _act("h", h, g, dev)
+    dout = _cotangent("dout", dout, g, dev)
+    dp, dst = _act("dout", dout, g, dev)
+    s0 = _state("initial_state", initial_state, (N, D), dev)
     if dfinal_state is not None:
         dfinal_state = dfinal_state.contiguous()
+    dsT = _state("dfinal_state", dfinal_state, (N, D), dev)
     if want_dinitial_state is None:
         want_dinitial_state = initial_state is not None
-    dx, dg = (torch.empty(g.shape, dtype=g.dtype, device=g.device) for _ in range(2))
+    dx, dg = _out("dx", None, g, dev), _out("dg", None, g, dev)
     ds0 = torch.empty((N, D), dtype=torch.float32, device=g.device) if want_dinitial_state else None
-    a = _abi.ScanBwdArgs(dt, gate, B, T, D, _ptr(x), 0 if x is None else _act("x", x, g), _ptr(g), _act("g", g, g),
-                         _ptr(h), _act("h", h, g), _ptr(dout), _act("dout", dout, g),
-                         _state("initial_state", initial_state, (N, D), g.device),
-                         _state("dfinal_state", dfinal_state, (N, D), g.device), _ptr(dx), _ptr(dg), _ptr(ds0), _ptr(cu),
-                         _ptr(cu_host), N, has_lb, lb)
-    ws = _scratch(lib.kda_gated_scan_bwd_workspace_size, a, workspace, g.device, "kda_gated_scan_bwd_workspace_size")  # noqa: F841
-    _launch(lib.kda_gated_scan_bwd, a, g.device, "kda_gated_scan_bwd")
+    _launch_scratch(call, (dt, gate, B, T, D, xp, xs, gp, gs, hp, hs, dp, dst, s0, dsT, dx.data_ptr(), dg.data_ptr(), _ptr(ds0), _ptr(cu),
+                           _ptr(cu_host), N, has_lb, lb), workspace, g.device, dev)
     return dx, dg, ds0

@@ -158,6 +158,30 @@ def test_norm_rows_of_a_fused_projection_and_in_place_sum():
         assert torch.equal(y2, y) and torch.equal(s2, s)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_of_heads_in_a_fused_projection(dtype):
+    """[B, T, H, D] views of slices, whose heads lie back to back and whose tokens do not."""
+    import kimi_delta_attention_20_b200 as kda
+    B, T, H, D = 2, 7, 3, 40
+    fused = draw(B, T, 3 * H * D + 5, dtype=dtype, seed=1)
+    x, g, r = (fused[..., k * H * D + 1:(k + 1) * H * D + 1].unflatten(-1, (H, D)) for k in range(3))
+    w = weights("f32", D, dtype, seed=2)
+    for kw in (dict(), dict(gate=g), dict(residual=r)):
+        a, b = kda.rms_norm(x, w, **kw), kda.rms_norm(x.contiguous(), w, **{k: v.contiguous() for k, v in kw.items()})
+        want = ref.norm(x, w, **kw)[0]
+        within("y", a if torch.is_tensor(a) else a[0], want, want.abs() * (half(dtype) + ref.norm_rel(D)))
+        if "residual" in kw:
+            assert torch.equal(a[1], b[1])
+    q, sc = kda.rms_norm_quant(x, w, gate=g, group_size=32)
+    assert q.shape == x.shape and sc.shape == (B, T, H, 2)
+    dx, dg, dw = kda.rms_norm_bwd(x, r, w, gate=g)
+    rx, rg, rw, mag, wmag = ref.norm_grads(x, r, w, g)
+    within("dx", dx, rx, rx.abs() * half(dtype) + mag * (54 * U + 2 * ref.norm_rel(D)))
+    within("dw", dw, rw, rw.abs() * half(w.dtype) + wmag * (50 * U + ref.norm_rel(D)))
+    with pytest.raises(ValueError):
+        kda.rms_norm(fused[..., :H * D].unflatten(-1, (H, D)).transpose(1, 2))
+
+
 def test_norm_empty_and_large_offsets():
     import kimi_delta_attention_20_b200 as kda
     x = torch.empty(0, 64, device=DEV)

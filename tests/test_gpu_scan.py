@@ -76,10 +76,24 @@ def test_scan_batch(N, T, form, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("lens,D", [([5000], 4), ([4700, 0, 300], 130), ([2500], 1000), ([700], 2600), ([300, 40], 20000), ([150], 39000)])
-def test_scan_over_many_chunks(lens, D, dtype):
-    """Chains of many chunks, in groups of 32 down to one chunk, with one and many channel tiles."""
+@pytest.mark.parametrize("lens,D", [([5000], 4), ([4700, 0, 300], 130), ([2500], 1000), ([700], 2600), ([300, 40], 20000), ([150], 39000),
+                                    ([300, 200, 100, 257], 8448), ([300, 200, 100, 257], 17024)])
+def test_scan_cut_along_time(lens, D, dtype):
+    """Sequences cut into many pieces, few, or none, with lanes of 8 and of 4 bytes."""
     check_scan(lens, D, dtype, FORMS[0], seed=D)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,T,D", [(1, 3000, 20), (3, 500, 260), (4, 300, 8448), (1000, 2, 64), (300, 7, 1024)])
+def test_scan_cut_of_a_batch(N, T, D, dtype):
+    check_scan([T] * N, D, dtype, FORMS[2], seed=N + T, span={})
+
+
+@pytest.mark.parametrize("lens", [[40, 0, 600, 1, 1, 1, 300], [0, 0, 900], [700, 0]], ids=str)
+def test_scan_with_offsets_on_the_device_alone(lens):
+    cu = torch.tensor(ref.bounds_of(lens), dtype=torch.int64, device=DEV)
+    for D in (16, 77, 4000):
+        check_scan(lens, D, torch.bfloat16, FORMS[0], seed=D, span=dict(cu_seqlens=cu))
 
 
 def test_scan_repeats_bit_for_bit():
