@@ -79,7 +79,6 @@ __global__ void __launch_bounds__(32) conv_fwd_kernel(const __grid_constant__ Co
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, C = p.C, R = p.span.R, units = (C + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
-    const bool full = c0 + TC <= C;
     const int b = min(piece * p.piece, R), e = piece + 1 == p.pieces ? R : min(b + p.piece, R);
     const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R)}, min(TC, C - c0) * (int)sizeof(T), lane};
 #pragma unroll 1
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(32) conv_fwd_kernel(const __grid_constant__ Co
             for (int k = 1; k < K; ++k) vfma(w[k], win[(j + k) % K], z, z);
 #pragma unroll
             for (int i = 0; i < W; ++i) z[i] *= sig<T>(z[i]);
-            put_row<G>(y + (long long)s * C, c, C, lane, full, z);
+            put_row<G>(y + (long long)s * C, c, C, lane, z);
         };
         // behind the last row of a sequence, its last K inputs in slots j, j + 1 ..
         auto close = [&](int row, int j) {
@@ -163,7 +162,6 @@ __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ Co
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, C = p.C, R = p.span.R, units = (C + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
-    const bool full = c0 + TC <= C;
     const int b = min(piece * p.piece, R), e = piece + 1 == p.pieces ? R : min(b + p.piece, R);
     const int stop = b < e ? min(e + K - 1, R) : e;  // rows that are walked
     const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R), walk_tensor<T>(p.dy, p.dy_stride, c0, C, R)},
@@ -202,7 +200,7 @@ __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ Co
                 vadd(v, f, v);
             }
             if (r >= q.start) {
-                put_row<G>(dx + (long long)r * C, c, C, lane, full, v);
+                put_row<G>(dx + (long long)r * C, c, C, lane, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < W; ++i)
@@ -255,7 +253,7 @@ __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ Co
                 for (int s = 0; s < S; ++s) {
                     one(s, s, true);
                     const int row = r + s - (K - 1);
-                    if (s >= K - 1 || row >= from) put_row<G>(dx + (long long)row * C, c, C, lane, full, acc[s % K]);
+                    if (s >= K - 1 || row >= from) put_row<G>(dx + (long long)row * C, c, C, lane, acc[s % K]);
                 }
                 rotate<K, W>(win, S % K);
                 rotate<K, W>(acc, S % K);

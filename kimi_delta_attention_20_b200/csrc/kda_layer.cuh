@@ -83,6 +83,7 @@ struct ScanCut {
     int lb;              // bytes of a lane
     int carries;         // whether a piece may continue a sequence of the one before
     void *maps;          // [pieces, channels of whole units] pairs (A, H): a piece as the map c -> A c + H
+    float *carry;        // [pieces, channels of whole units] states before the pieces, or null
 };
 
 struct ScanParams {

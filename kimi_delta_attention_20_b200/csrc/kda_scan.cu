@@ -4,19 +4,20 @@
 // its backward pass and its single token.
 //
 // Bound by HBM: 6 bytes an element forward, 10 backward (bf16; 12 in the sigmoid form).
-// A walker -- one warp -- walks 128 bytes of channels (64 in bf16, 32 in fp32) down the
-// rows with the states in registers; asynchronous copies run several stages of 16 rows
-// ahead of it into its shared memory, and six walkers share an SM, so about 170 KB an SM
-// are in flight. Each element is read once, decayed once (about nine instructions) and
-// written once, and nothing waits for another CTA.
+// Each element is read once, decayed once and written once by a walker, which carries the
+// states of its channels in registers; seven walkers share an SM, and nothing waits for
+// another CTA.
 //
 // Where channels times sequences are too few to fill the GPU, time is cut too. A run of
 // rows is the map c -> A c + H of the state before it (A the product of its a, H its result
 // from zero; a sequence's first row drops what came before): a first kernel reduces each
 // piece to its map, and the walker of a piece composes the maps of the pieces before it,
-// back to where its sequence began, before it starts. That reads x and g a second time
-// (mostly from L2 where they fit). A single pass that hands states from CTA to CTA
-// measured worse: 768 us against 219 us ... see the table of the cuts at scan_cut.
+// back to where its sequence began, before it starts. That reads two of the tensors a second
+// time, from L2 where they fit. Handing states from CTA to CTA inside one kernel would read
+// once, but measured slower: links of a chain have to wait for one another, and every row is
+// walked twice by the CTA that holds it (31744 x 12288: 768 us; 8192 x 2048 backward: 82
+// against 47; with flags behind fences a handover alone took 8 us under load). What is
+// composed, and in which order, goes by the shapes: results do not depend on timing.
 #include <type_traits>
 
 #include "kda_layer.cuh"
@@ -25,11 +26,14 @@ namespace kda {
 
 namespace {
 
-// Walkers that run at the same time, with rings of about 30 KiB.
+// Walkers that run at the same time, with rings of 24 KiB.
 constexpr int kWalkerSlots = 148 * 7;
 constexpr int kMinPiece = 64;       // rows of a piece, at least
 constexpr int kStage = 8;  // rows of a stage
-constexpr int ring_stages(int lb, int tensors) { return 120 / lb / tensors; }
+constexpr int ring_stages(int lb, int tensors) { return 96 / lb / tensors; }
+// Rows that are unrolled: a stage, or two where a row of single elements takes so many
+// instructions that a stage of them would not stay in the instruction cache.
+template <int G> constexpr int unrolled() { return G > 2 ? kStage : 2; }
 template <typename T, int G, int LB, int N> using ScanRing = Ring<T, G, LB, kStage, N, ring_stages(LB, N)>;
 
 // a of the gate input, and the weight b of x in the sigmoid form: 1 - a without the
@@ -127,6 +131,71 @@ __device__ __forceinline__ void compose(const Map<W> *at, long long pitch, int f
     }
 }
 
+// The state before every piece, where pieces are many: a CTA takes a channel unit, its 32
+// warps a run of pieces each. They compose their maps, then the runs before their own, and
+// walk their maps again.
+template <int W>
+__global__ void __launch_bounds__(1024) scan_carry_kernel(const void *maps, float *carry, int pieces, int units, int backward) {
+    __shared__ Map<W> runs[32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long pitch = (long long)units * 32, at = (long long)blockIdx.x * 32 + lane;
+    const Map<W> *m = static_cast<const Map<W> *>(maps) + at;
+    const int per = (pieces + 31) / 32, p0 = min(warp * per, pieces), p1 = min(p0 + per, pieces);
+    auto place = [&](int j) { return (long long)(backward ? pieces - 1 - j : j) * pitch; };
+    Map<W> run;
+#pragma unroll
+    for (int i = 0; i < W; ++i) run.ch[i] = make_float2(1.f, 0.f);
+    for (int j = p0; j < p1; j += 4) {
+        Map<W> q[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < p1) q[u] = m[place(j + u)];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < p1)
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const float2 n = q[u].ch[i];
+                    run.ch[i] = n.x < 0.f ? n : make_float2(run.ch[i].x < 0.f ? -1.f : run.ch[i].x * n.x, fmaf(n.x, run.ch[i].y, n.y));
+                }
+    }
+    runs[warp][lane] = run;
+    __syncthreads();
+    float c[W];
+    vset(c, 0.f);
+    auto through = [&](const Map<W> &n) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) c[i] = n.ch[i].x < 0.f ? n.ch[i].y : fmaf(n.ch[i].x, c[i], n.ch[i].y);
+    };
+    for (int w = 0; w < warp; ++w) through(runs[w][lane]);
+    for (int j = p0; j < p1; j += 4) {
+        Map<W> q[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < p1) q[u] = m[place(j + u)];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u < p1) {
+#pragma unroll
+                for (int i = 0; i < W; ++i) carry[(place(j + u) + at) * W + i] = c[i];
+                through(q[u]);
+            }
+    }
+}
+
+// The state before (backward: behind) a piece, from the carry kernel or composed here of the
+// maps from piece `first` on.
+template <int W>
+__device__ __forceinline__ void enter(const ScanCut &cut, int c0, int units, int first, int piece, int step, float (&c)[W]) {
+    if (!cut.carry) {
+        compose(lane_map<W>(cut, c0), (long long)units * 32, first, piece, step, c);
+        return;
+    }
+    const float *p = cut.carry + ((long long)piece * units * 32 + c0 / W) * W;
+#pragma unroll
+    for (int i = 0; i < W; ++i) c[i] = p[i];
+}
+
 // ---------------------------------------------------------------- forward
 // One step of a lane's channels: a, and what is added to a h.
 template <typename T, bool SIG, typename R, int W>
@@ -142,11 +211,10 @@ __device__ __forceinline__ void step_fwd(const R &ring, int slot, int s, int r, 
 template <typename T, int G, int LB, bool SIG>
 __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ ScanParams p) {
     using RN = ScanRing<T, G, LB, 2>;
-    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), TC = walk_channels<T, LB>();
+    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), UN = unrolled<G>(), TC = walk_channels<T, LB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, D = p.D, R = p.span.R, units = (D + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
-    const bool full = c0 + TC <= D;
     int b, e;
     piece_rows(p.cut, p.span, piece, b, e);
     const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, D, R), walk_tensor<T>(p.g, p.g_stride, c0, D, R)},
@@ -166,7 +234,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
     if (b >= e) return;
     Seq q = seq_of(p.span, b, lane);
     float h[W];
-    if (q.start < b) compose(lane_map<W>(p.cut, c), (long long)units * 32, piece_of(p.cut, p.span, q.start), piece, 1, h);
+    if (q.start < b) enter(p.cut, c, units, piece_of(p.cut, p.span, q.start), piece, 1, h);
     else get_state(p.s0, q.n, c, D, h);
     // behind the last row of a sequence
     auto close = [&](int row) {
@@ -189,16 +257,24 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
             float a[W], v[W];
             step_fwd<T, SIG>(ring, slot, s, r + s, p.lb, a, v);
             vfma(a, h, v, h);
-            put_row<G>(out + (long long)s * D, c, D, lane, full, h);
+            put_row<G>(out + (long long)s * D, c, D, lane, h);
         };
         if (min(q.end, e) >= r + S) {
-            float a[S][W], v[S][W];
+            auto rows = [&](int s0) {  // the decays of UN rows, then the rows
+                float a[UN][W], v[UN][W];
 #pragma unroll
-            for (int s = 0; s < S; ++s) step_fwd<T, SIG>(ring, slot, s, r + s, p.lb, a[s], v[s]);
+                for (int s = 0; s < UN; ++s) step_fwd<T, SIG>(ring, slot, s0 + s, r + s0 + s, p.lb, a[s], v[s]);
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                vfma(a[s], h, v[s], h);
-                put_row<G>(out + (long long)s * D, c, D, lane, full, h);
+                for (int s = 0; s < UN; ++s) {
+                    vfma(a[s], h, v[s], h);
+                    put_row<G>(out + (long long)(s0 + s) * D, c, D, lane, h);
+                }
+            };
+            if constexpr (UN == S) {
+                rows(0);
+            } else {
+#pragma unroll 1
+                for (int s0 = 0; s0 < S; s0 += UN) rows(s0);
             }
             if (q.end == r + S) close(r + S);
         } else {
@@ -219,7 +295,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
 template <typename T, int G, int LB, bool SIG>
 __global__ void __launch_bounds__(32) scan_reduce_kernel(const __grid_constant__ ScanParams p) {
     using RN = ScanRing<T, G, LB, 2>;
-    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), TC = walk_channels<T, LB>();
+    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), UN = unrolled<G>(), TC = walk_channels<T, LB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, D = p.D, R = p.span.R, units = (D + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
@@ -260,13 +336,21 @@ __global__ void __launch_bounds__(32) scan_reduce_kernel(const __grid_constant__
             vmul(A, a, A);
         };
         if (e >= r + S) {
-            float a[S][W], v[S][W];
+            auto rows = [&](int s0) {
+                float a[UN][W], v[UN][W];
 #pragma unroll
-            for (int s = 0; s < S; ++s) step_fwd<T, SIG>(ring, slot, s, r + s, p.lb, a[s], v[s]);
+                for (int s = 0; s < UN; ++s) step_fwd<T, SIG>(ring, slot, s0 + s, r + s0 + s, p.lb, a[s], v[s]);
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                vfma(a[s], h, v[s], h);
-                vmul(A, a[s], A);
+                for (int s = 0; s < UN; ++s) {
+                    vfma(a[s], h, v[s], h);
+                    vmul(A, a[s], A);
+                }
+            };
+            if constexpr (UN == S) {
+                rows(0);
+            } else {
+#pragma unroll 1
+                for (int s0 = 0; s0 < S; s0 += UN) rows(s0);
             }
         } else {
 #pragma unroll 1
@@ -292,11 +376,10 @@ template <typename T, int G, int LB, bool SIG>
 __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ ScanBwdParams p) {
     constexpr int N = SIG ? 4 : 3;
     using RN = ScanRing<T, G, LB, N>;
-    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, N), TC = walk_channels<T, LB>();
+    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, N), UN = unrolled<G>(), TC = walk_channels<T, LB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, D = p.D, R = p.span.R, units = (D + TC - 1) / TC;
     const int place = blockIdx.x / units, piece = p.cut.pieces - 1 - place, c0 = (blockIdx.x - place * units) * TC, c = c0 + lane * W;
-    const bool full = c0 + TC <= D;
     int b, e;
     piece_rows(p.cut, p.span, piece, b, e);
     RN ring{dyn, {walk_tensor<T>(p.g, p.g_stride, c0, D, R), walk_tensor<T>(p.dout, p.dout_stride, c0, D, R),
@@ -320,7 +403,7 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
     if (b >= e) return;
     Seq q = seq_of(p.span, e - 1, lane);
     float k[W];
-    if (q.end > e) compose(lane_map<W>(p.cut, c), (long long)units * 32, piece_of(p.cut, p.span, q.end - 1), piece, -1, k);
+    if (q.end > e) enter(p.cut, c, units, piece_of(p.cut, p.span, q.end - 1), piece, -1, k);
     else get_state(p.dsT, q.n, c, D, k);
     int slot = 0, next = ST - 1;
 #pragma unroll 1
@@ -354,11 +437,11 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
                 for (int i = 0; i < W; ++i)
                     if (g[i] < p.lb) dg[i] = 0.f;
             }
-            put_row<G>(static_cast<T *>(p.dx) + (long long)row * D, c, D, lane, full, d);
-            put_row<G>(static_cast<T *>(p.dg) + (long long)row * D, c, D, lane, full, dg);
+            put_row<G>(static_cast<T *>(p.dx) + (long long)row * D, c, D, lane, d);
+            put_row<G>(static_cast<T *>(p.dg) + (long long)row * D, c, D, lane, dg);
         };
         if (r >= b && q.start < r) {
-#pragma unroll
+#pragma unroll(UN)
             for (int s = S - 1; s >= 0; --s) one(s, false);
         } else {
 #pragma unroll 1
@@ -383,7 +466,7 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
 template <typename T, int G, int LB, bool SIG>
 __global__ void __launch_bounds__(32) scan_reduce_bwd_kernel(const __grid_constant__ ScanBwdParams p) {
     using RN = ScanRing<T, G, LB, 2>;
-    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), TC = walk_channels<T, LB>();
+    constexpr int W = RN::W, S = kStage, ST = ring_stages(LB, 2), UN = unrolled<G>(), TC = walk_channels<T, LB>();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, D = p.D, R = p.span.R, units = (D + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
@@ -428,7 +511,7 @@ __global__ void __launch_bounds__(32) scan_reduce_bwd_kernel(const __grid_consta
             vmul(A, a, A);
         };
         if (r >= b) {
-#pragma unroll
+#pragma unroll(UN)
             for (int s = S - 1; s >= 0; --s) one(s);
         } else {
 #pragma unroll 1
@@ -533,6 +616,19 @@ ScanCut cut_for(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int
     return c;
 }
 
+// A walker composes up to this many maps itself; beyond, a kernel between the two passes
+// hands every walker its state: it takes 7 us, which 64 pieces do not repay (8192 x 2048
+// backward: 48 us without, 55 with it) and 518 do (131072 x 256 in bf16: 105 without, 85).
+constexpr int kOwnMaps = 256;
+
+// Scratch: the maps, then the states before the pieces.
+size_t map_bytes(const ScanCut &c, int D, bool bf16) { return sizeof(float2) * (size_t)c.pieces * units_of(D, bf16, c.lb) * (bf16 ? 16 : 8) * c.lb; }
+
+void lay_out(ScanCut *c, int D, bool bf16, void *workspace) {
+    c->maps = workspace;
+    c->carry = c->carries && c->pieces > kOwnMaps ? reinterpret_cast<float *>(static_cast<char *>(workspace) + map_bytes(*c, D, bf16)) : nullptr;
+}
+
 // Lanes of 8 bytes take about two thirds of the instructions an element; lanes of 4 make
 // twice the walkers, and are taken where they save the cut along time (31744 x 12288 packed
 // of four sequences: 490 us in one pass, against 637 with lanes of 8 in two).
@@ -552,15 +648,25 @@ template <typename T, typename P> cudaError_t run_walk(void (*kernel)(P), const 
     return cudaGetLastError();
 }
 
+template <int W> cudaError_t run_carry(const ScanCut &c, int D, bool bf16, int backward, cudaStream_t st) {
+    if (!c.carry) return cudaSuccess;
+    const int units = units_of(D, bf16, c.lb);
+    count_launch();
+    scan_carry_kernel<W><<<units, 1024, 0, st>>>(c.maps, c.carry, c.pieces, units, backward);
+    return cudaGetLastError();
+}
+
 template <typename T, int G, int LB, bool SIG> cudaError_t run_fwd_lb(const ScanParams &p, cudaStream_t st) {
     constexpr int ring = ScanRing<T, G, LB, 2>::BYTES;
     cudaError_t e = cudaSuccess;
     if (p.cut.carries) e = run_walk<T>(scan_reduce_kernel<T, G, LB, SIG>, p, ring, st);
+    if (e == cudaSuccess) e = run_carry<lane_channels<T, LB>()>(p.cut, p.D, sizeof(T) == 2, 0, st);
     return e != cudaSuccess ? e : run_walk<T>(scan_fwd_kernel<T, G, LB, SIG>, p, ring, st);
 }
 template <typename T, int G, int LB, bool SIG> cudaError_t run_bwd_lb(const ScanBwdParams &p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     if (p.cut.carries) e = run_walk<T>(scan_reduce_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, 2>::BYTES, st);
+    if (e == cudaSuccess) e = run_carry<lane_channels<T, LB>()>(p.cut, p.D, sizeof(T) == 2, 1, st);
     return e != cudaSuccess ? e : run_walk<T>(scan_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, SIG ? 4 : 3>::BYTES, st);
 }
 // Lanes of 4 bytes come with 16-byte accesses only (see scan_cut).
@@ -599,7 +705,9 @@ template <typename T, bool AL, bool SIG> cudaError_t run_step(const ScanStepPara
 size_t scan_workspace_bytes(const RowSpan &span, const int32_t *cu_host, int D, bool bf16) {
     // of the wider walkers: whether the narrower are taken goes by alignment too
     const ScanCut c = cut_for(span, cu_host, D, bf16, 8);
-    return c.carries ? sizeof(float2) * (size_t)c.pieces * units_of(D, bf16, 8) * (bf16 ? 128 : 64) : 0;
+    if (!c.carries) return 0;
+    const size_t maps = map_bytes(c, D, bf16);
+    return c.pieces > kOwnMaps ? maps + maps / 2 : maps;
 }
 
 cudaError_t launch_scan(ScanParams p, const int32_t *cu_host, bool bf16, bool sigmoid, void *workspace, cudaStream_t st) {
@@ -609,7 +717,7 @@ cudaError_t launch_scan(ScanParams p, const int32_t *cu_host, bool bf16, bool si
     ac.rows(p.g, p.g_stride, p.D, esz);
     ac.rows(p.h, p.D, p.D, esz);
     p.cut = scan_cut(p.span, cu_host, p.D, bf16, ac.g());
-    p.cut.maps = workspace;
+    lay_out(&p.cut, p.D, bf16, workspace);
     KDA_SCAN_PICK(run_fwd, p, bf16, ac.g(), sigmoid, st)
 }
 
@@ -623,7 +731,7 @@ cudaError_t launch_scan_bwd(ScanBwdParams p, const int32_t *cu_host, bool bf16, 
     ac.rows(p.dx, p.D, p.D, esz);
     ac.rows(p.dg, p.D, p.D, esz);
     p.cut = scan_cut(p.span, cu_host, p.D, bf16, ac.g());
-    p.cut.maps = workspace;
+    lay_out(&p.cut, p.D, bf16, workspace);
     KDA_SCAN_PICK(run_bwd, p, bf16, ac.g(), sigmoid, st)
 }
 

@@ -187,11 +187,12 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
             const char *src = t[i].at + (long long)(row + lr) * t[i].stride + lc;
             const unsigned d = (unsigned)__cvta_generic_to_shared(to + lr * PITCH + lc);
             const long long step = ROWS * t[i].stride;
-            if (inner && width == ROW) {
+            if (inner) {
 #pragma unroll
                 for (int k = 0; k < S; k += ROWS, src += step)
 #pragma unroll
-                    for (int j = 0; j < ROUNDS; ++j) copy<G>(d + k * PITCH + j * 32 * G, src + j * 32 * G);
+                    for (int j = 0; j < ROUNDS; ++j)
+                        if (lc + j * 32 * G < width) copy<G>(d + k * PITCH + j * 32 * G, src + j * 32 * G);
                 return;
             }
 #pragma unroll 1
@@ -205,15 +206,14 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
         } else {
             constexpr int WORDS = PITCH / 16, COUNT = S * WORDS;
             // only words of the tensor's first and last rows may reach beyond it
-            const bool plain = row > lo && row + S < hi && width == ROW;
+            const bool plain = row > lo && row + S < hi;
             if (plain) {
 #pragma unroll
                 for (int q = 0; q < (COUNT + 31) / 32; ++q) {
                     const int x = q * 32 + lane, k = x / WORDS, j = x - k * WORDS;
                     const char *a = t[i].at + (long long)(row + k) * t[i].stride;
                     const int off = (int)((uint32_t)reinterpret_cast<uintptr_t>(a) & 15u);
-                    // the last word of a row that begins on a boundary is none of its
-                    if (x < COUNT && (j < WORDS - 1 || off)) copy<16>((unsigned)__cvta_generic_to_shared(to + x * 16), a - off + 16 * j);
+                    if (x < COUNT && 16 * j - off < width) copy<16>((unsigned)__cvta_generic_to_shared(to + x * 16), a - off + 16 * j);
                 }
                 return;
             }
@@ -254,8 +254,7 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
 };
 
 // Stores the lane's channels, from c on, of an output row (the whole warp takes part).
-// full: all the channels of the walker are below C.
-template <int G, int W> __device__ __forceinline__ void put_row(float *row, int c, int C, int, bool, const float (&v)[W]) {
+template <int G, int W> __device__ __forceinline__ void put_row(float *row, int c, int C, int, const float (&v)[W]) {
     if constexpr (G >= 8 && W == 2) {
         if (c < C) *reinterpret_cast<float2 *>(row + c) = make_float2(v[0], v[1]);
     } else {
@@ -264,17 +263,13 @@ template <int G, int W> __device__ __forceinline__ void put_row(float *row, int 
             if (c + i < C) row[c + i] = v[i];
     }
 }
-template <int G, int W> __device__ __forceinline__ void put_row(__nv_bfloat16 *row, int c, int C, int lane, bool full, const float (&v)[W]) {
+template <int G, int W> __device__ __forceinline__ void put_row(__nv_bfloat16 *row, int c, int C, int lane, const float (&v)[W]) {
     if constexpr (G >= 8 && W == 4) {
         if (c < C) *reinterpret_cast<uint2 *>(row + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     } else if constexpr (G >= 4) {
 #pragma unroll
         for (int i = 0; i < W; i += 2)
             if (c + i < C) *reinterpret_cast<uint32_t *>(row + c + i) = pack_bf16(v[i], v[i + 1]);
-    } else if (!full) {
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (c + i < C) row[c + i] = __float2bfloat16_rn(v[i]);
     } else {
         // where the row begins in the middle of a word, words pair a lane's last channel with the next lane's first
         const bool odd = reinterpret_cast<uintptr_t>(row) & 2;
@@ -283,12 +278,17 @@ template <int G, int W> __device__ __forceinline__ void put_row(__nv_bfloat16 *r
 #pragma unroll
         for (int i = W - 1; i > 0; --i) x[i] = odd ? v[i - 1] : v[i];
         if (!odd) x[0] = v[0];
-        uint32_t *w = reinterpret_cast<uint32_t *>(row + (odd ? c - 1 : c));
+        const int at = odd ? c - 1 : c;
+        __nv_bfloat16 *p = row + at;
+        const bool edge = odd && lane == 0;  // its first word is shared with the tile before
 #pragma unroll
-        for (int i = 0; i < W; i += 2)
-            if (i > 0 || lane > 0 || !odd) w[i / 2] = pack_bf16(x[i], x[i + 1]);
-        if (odd && lane == 0) row[c] = __float2bfloat16_rn(v[0]);
-        if (odd && lane == 31) row[c + W - 1] = __float2bfloat16_rn(v[W - 1]);
+        for (int i = 0; i < W; i += 2) {
+            const uint32_t q = pack_bf16(x[i], x[i + 1]);
+            if (at + i + 1 < C && !(edge && i == 0)) *reinterpret_cast<uint32_t *>(p + i) = q;
+            else if (at + i < C && !(edge && i == 0)) *reinterpret_cast<uint16_t *>(p + i) = (uint16_t)q;
+        }
+        if (edge && c < C) row[c] = __float2bfloat16_rn(v[0]);
+        if (odd && lane == 31 && c + W - 1 < C) row[c + W - 1] = __float2bfloat16_rn(v[W - 1]);
     }
 }
 

@@ -239,7 +239,10 @@ def _norm(x, weight, residual, gate, eps, residual_out, quant=None, out=None):
         group, pow2, scales = quant
         if group not in (0, 32, 64, 128):
             raise ValueError("group_size must be 0 (the whole row), 32, 64 or 128")
-        y = _out_as("out", out, x.shape, torch.float8_e4m3fn, x.device, dev)
+        if out is None and x.is_contiguous():
+            y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+        else:
+            y = _out_as("out", out, x.shape, torch.float8_e4m3fn, x.device, dev)
         shape = (*x.shape[:-1], -(-D // group) if group else 1)
         scales = _out_as("scales_out", scales, shape, torch.float32, x.device, dev)
     _launch(call, call.pack(dt, wdt, x.numel() // D if D else 0, heads, D, xp, xs, rp, rs, gp, gs, wp, eps, y.data_ptr(),
