@@ -357,14 +357,15 @@ KDA_API kda_status kda_chunk_fwd_noalloc_status(const kda_chunk_args *args, void
  *  - Activations are rows of channels whose channels are contiguous; `*_stride`
  *    is the distance between rows in elements (at least the row's length; 0 means
  *    dense), so a slice of a fused projection is read in place. Outputs are dense.
- *  - Pointers need the alignment of their element only; rows that are aligned to
- *    16 bytes (8 bytes for four bf16) with a channel count that is a multiple of
- *    eight (four for the convolution and the scan) run wider accesses.
+ *  - Pointers need the alignment of their element only. Rows are accessed by the
+ *    largest of 16, 8, 4 and 2 bytes that divides the pointers, strides and row
+ *    lengths of a call's activations; 16 is the fastest.
+ *  - Up to 2^28 channels (the norm: 16384) and 2^31 - 4097 rows.
  *  - Packed sequences as in kda_chunk_args: with cu_seqlens B must be 1 and
  *    cu_seqlens_host, when given, is validated; without it the device copy is
  *    trusted (it moves no access out of the buffers, whatever it holds).
- *  - An output that overlaps an input or another output is refused, except where
- *    stated.
+ *  - An output or workspace that overlaps an input or another output is refused,
+ *    except where stated.
  *  - Sums, norms, states and convolution windows are fp32.
  */
 
@@ -551,8 +552,8 @@ typedef struct {
  * workspace each. */
 KDA_API kda_status kda_gated_scan_workspace_size(const kda_scan_args *args, size_t *bytes);
 
-/* Queue the recurrence on `stream`: one launch, or two where sequences are cut along time
- * to fill the GPU (results depend on the shapes alone, not on timing). */
+/* Queue the recurrence on `stream`: one launch, or two or three where sequences are cut
+ * along time to fill the GPU (results depend on the shapes alone, not on timing). */
 KDA_API kda_status kda_gated_scan(const kda_scan_args *args, void *stream);
 
 /* One token of N sequences: state <- a state + x (or (1 - a) x), h = state. */

@@ -82,7 +82,8 @@ struct ScanCut {
     int kind, pieces, per, rows;
     int lb;              // bytes of a lane
     int carries;         // whether a piece may continue a sequence of the one before
-    void *maps;          // [pieces, channels of whole units] pairs (A, H): a piece as the map c -> A c + H
+    void *maps;          // [pieces, channels of whole units] pairs (A, H): a piece as the map c -> A c + H;
+                         // null where no piece carries
     float *carry;        // [pieces, channels of whole units] states before the pieces, or null
 };
 
@@ -122,7 +123,7 @@ struct ScanStepParams {
 
 cudaError_t launch_rms_norm(const NormParams &p, bool bf16, cudaStream_t st);
 cudaError_t launch_rms_norm_quant(const NormParams &p, bool bf16, int g, cudaStream_t st);
-size_t rms_norm_bwd_workspace_bytes(long long rows, int D, bool bf16, bool weight);
+size_t rms_norm_bwd_workspace_bytes(long long rows, int D, bool weight);
 cudaError_t launch_rms_norm_bwd(const NormBwdParams &p, bool bf16, cudaStream_t st);
 
 cudaError_t launch_conv(ConvParams p, bool bf16, cudaStream_t st);

@@ -14,6 +14,7 @@ bool token_conv_supported(int K);   // kda_token.cu
 namespace {
 
 constexpr int kMaxNormDim = 16384;
+constexpr int kMaxChannels = 1 << 28;
 
 kda_status launched(cudaError_t e) {
     if (e == cudaSuccess) return KDA_OK;
@@ -53,6 +54,9 @@ struct Checker {
         if (!p) { bad |= need; return; }
         if (reinterpret_cast<uintptr_t>(p) % (align ? align : esz)) { bad = true; return; }
         out[nout++] = range(p, rows, cols, cols, esz);
+    }
+    void scratch(const void *p, size_t need) {
+        if (p && need) out[nout++] = range(p, 1, (long long)need, (long long)need, 1);
     }
     static bool overlap(const Range &a, const Range &b) { return a.lo < b.hi && b.lo < a.hi; }
     // Whether every output stands apart from the inputs and the other outputs.
@@ -118,13 +122,13 @@ kda_status check_norm_shape(int dtype, int weight_dtype, long long rows, int hea
 }
 
 kda_status check_conv_shape(int dtype, int C, int K) {
-    if (!dtype_ok(dtype) || C < 1) return KDA_ERR_INVALID_ARGUMENT;
+    if (!dtype_ok(dtype) || C < 1 || C > kMaxChannels) return KDA_ERR_INVALID_ARGUMENT;
     if (!kda::token_conv_supported(K)) return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 
 template <typename Args> kda_status scan_shape(const Args *a, kda::RowSpan *span) {
-    if (!dtype_ok(a->dtype) || a->D < 1) return KDA_ERR_INVALID_ARGUMENT;
+    if (!dtype_ok(a->dtype) || a->D < 1 || a->D > kMaxChannels) return KDA_ERR_INVALID_ARGUMENT;
     kda_status s = check_scan_gate(a->gate, a->has_lower_bound, a->lower_bound);
     if (s != KDA_OK) return s;
     return check_span(a->B, a->T, a->N, a->cu_seqlens, a->cu_seqlens_host, span);
@@ -190,7 +194,7 @@ kda_status kda_rms_norm_bwd_workspace_size(const kda_rms_norm_bwd_args *a, size_
     if (!a || !bytes) return KDA_ERR_INVALID_ARGUMENT;
     kda_status s = check_norm_shape(a->dtype, a->weight_dtype, a->rows, a->heads, a->D, a->eps);
     if (s != KDA_OK) return s;
-    *bytes = kda::rms_norm_bwd_workspace_bytes(a->rows, a->D, a->dtype == KDA_DTYPE_BF16, a->dweight != nullptr);
+    *bytes = kda::rms_norm_bwd_workspace_bytes(a->rows, a->D, a->dweight != nullptr);
     return KDA_OK;
 }
 
@@ -212,6 +216,7 @@ kda_status kda_rms_norm_bwd(const kda_rms_norm_bwd_args *a, void *stream) {
     c.output(a->dx, a->rows > 0, a->rows, a->D, esz);
     c.output(a->dgate, a->rows > 0 && a->gate, a->rows, a->D, esz);
     c.output(a->dweight, false, 1, a->D, wsz);
+    c.scratch(a->workspace, need);
     if (c.bad || !c.apart() || (a->dgate && !a->gate) || (a->dweight && !a->weight)) return KDA_ERR_INVALID_ARGUMENT;
     if (a->rows == 0) {  // a sum over no rows
         if (!a->dweight) return KDA_OK;
@@ -294,6 +299,7 @@ kda_status kda_causal_conv_bwd(const kda_conv_bwd_args *a, void *stream) {
     c.output(a->dx, any, p.span.R, a->C, esz);
     c.output(a->dconv_w, false, a->C, a->K, 4);
     c.output(a->dinitial_state, false, p.span.N, state, 4);
+    c.scratch(a->workspace, need);
     if (c.bad || !c.apart()) return KDA_ERR_INVALID_ARGUMENT;
     if (!workspace_ok(a->workspace, a->workspace_bytes, need, 16)) return KDA_ERR_WORKSPACE;
     if (!any && !a->dconv_w && !a->dinitial_state) return KDA_OK;
@@ -320,6 +326,7 @@ kda_status kda_gated_scan(const kda_scan_args *a, void *stream) {
     c.input(a->initial_state, false, p.span.N, a->D, 0, 4);
     c.output(a->h, any, p.span.R, a->D, esz);
     c.output(a->final_state, false, p.span.N, a->D, 4);
+    c.scratch(a->workspace, need);
     if (c.bad || !c.apart()) return KDA_ERR_INVALID_ARGUMENT;
     if (!workspace_ok(a->workspace, a->workspace_bytes, need, 16)) return KDA_ERR_WORKSPACE;
     if (!any && !a->final_state) return KDA_OK;
@@ -330,7 +337,7 @@ kda_status kda_gated_scan(const kda_scan_args *a, void *stream) {
 }
 
 kda_status kda_gated_scan_step(const kda_scan_step_args *a, void *stream) {
-    if (!a || !dtype_ok(a->dtype) || a->N < 0 || a->D < 1) return KDA_ERR_INVALID_ARGUMENT;
+    if (!a || !dtype_ok(a->dtype) || a->N < 0 || a->D < 1 || a->D > kMaxChannels) return KDA_ERR_INVALID_ARGUMENT;
     kda_status s = check_scan_gate(a->gate, a->has_lower_bound, a->lower_bound);
     if (s != KDA_OK) return s;
     if (a->N == 0) return KDA_OK;
@@ -372,6 +379,7 @@ kda_status kda_gated_scan_bwd(const kda_scan_bwd_args *a, void *stream) {
     c.output(a->dx, any, p.span.R, a->D, esz);
     c.output(a->dg, any, p.span.R, a->D, esz);
     c.output(a->dinitial_state, false, p.span.N, a->D, 4);
+    c.scratch(a->workspace, need);
     if (c.bad || !c.apart()) return KDA_ERR_INVALID_ARGUMENT;
     if (!workspace_ok(a->workspace, a->workspace_bytes, need, 16)) return KDA_ERR_WORKSPACE;
     if (!any && !a->dinitial_state) return KDA_OK;

@@ -123,7 +123,7 @@ template <typename T, int G, int TPR, int NU> struct Bwd {
 
 }  // namespace
 
-size_t rms_norm_bwd_workspace_bytes(long long rows, int D, bool, bool weight) {
+size_t rms_norm_bwd_workspace_bytes(long long rows, int D, bool weight) {
     return weight ? sizeof(float) * (size_t)norm_ctas(rows, bwd_shape(rows, D), true) * D : 0;
 }
 

@@ -29,7 +29,7 @@ namespace {
 // Walkers that run at the same time, with rings of 24 KiB.
 constexpr int kWalkerSlots = 148 * 7;
 constexpr int kMinPiece = 64;       // rows of a piece, at least
-constexpr int kStage = 8;  // rows of a stage
+constexpr int kStage = 8;           // rows of a stage
 constexpr int ring_stages(int lb, int tensors) { return 96 / lb / tensors; }
 // Rows that are unrolled: a stage, or two where a row of single elements takes so many
 // instructions that a stage of them would not stay in the instruction cache.
@@ -184,9 +184,14 @@ __global__ void __launch_bounds__(1024) scan_carry_kernel(const void *maps, floa
 }
 
 // The state before (backward: behind) a piece, from the carry kernel or composed here of the
-// maps from piece `first` on.
+// maps from piece `first` on. Without maps (a cut after the host's offsets, none of which the
+// device's may share) zeros.
 template <int W>
 __device__ __forceinline__ void enter(const ScanCut &cut, int c0, int units, int first, int piece, int step, float (&c)[W]) {
+    if (!cut.maps) {
+        vset(c, 0.f);
+        return;
+    }
     if (!cut.carry) {
         compose(lane_map<W>(cut, c0), (long long)units * 32, first, piece, step, c);
         return;
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
     RN ring{dyn, {walk_tensor<T>(p.g, p.g_stride, c0, D, R), walk_tensor<T>(p.dout, p.dout_stride, c0, D, R),
                   walk_tensor<T>(p.h, p.h_stride, c0, D, R)}, min(TC, D - c0) * (int)sizeof(T), lane};
     if (SIG) ring.t[N - 1] = walk_tensor<T>(p.x, p.x_stride, c0, D, R);
-    // a stage holds rows row .. row+15, of h the rows before them
+    // a stage's rows from `row` on, of h the rows before them
     auto load = [&](int slot, int row) {
         ring.load(slot, 0, row, b, e);
         ring.load(slot, 1, row, b, e);
@@ -625,13 +630,13 @@ constexpr int kOwnMaps = 256;
 size_t map_bytes(const ScanCut &c, int D, bool bf16) { return sizeof(float2) * (size_t)c.pieces * units_of(D, bf16, c.lb) * (bf16 ? 16 : 8) * c.lb; }
 
 void lay_out(ScanCut *c, int D, bool bf16, void *workspace) {
-    c->maps = workspace;
+    c->maps = c->carries ? workspace : nullptr;
     c->carry = c->carries && c->pieces > kOwnMaps ? reinterpret_cast<float *>(static_cast<char *>(workspace) + map_bytes(*c, D, bf16)) : nullptr;
 }
 
 // Lanes of 8 bytes take about two thirds of the instructions an element; lanes of 4 make
 // twice the walkers, and are taken where they save the cut along time (31744 x 12288 packed
-// of four sequences: 490 us in one pass, against 637 with lanes of 8 in two).
+// of four sequences: 500 us in one pass, against 637 with lanes of 8 in two).
 ScanCut scan_cut(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int g) {
     const ScanCut wide = cut_for(sp, cu_host, D, bf16, 8);
     if (!wide.carries || g < 16) return wide;

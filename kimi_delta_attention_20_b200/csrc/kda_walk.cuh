@@ -209,8 +209,9 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
             }
         } else {
             constexpr int WORDS = PITCH / 16, COUNT = S * WORDS;
-            // only words of the tensor's first and last rows may reach beyond it
-            const bool plain = row > lo && row + S < hi;
+            // words near the tensor's first and last rows may reach beyond it
+            const char *from = t[i].at + (long long)row * t[i].stride;
+            const bool plain = inner && from - 14 >= t[i].begin && from + (S - 1) * t[i].stride + width + 14 <= t[i].end;
             if (plain) {
 #pragma unroll
                 for (int q = 0; q < (COUNT + 31) / 32; ++q) {

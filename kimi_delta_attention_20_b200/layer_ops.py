@@ -165,6 +165,11 @@ def _span(x, cu_seqlens, cu_seqlens_cpu, features):
     return B, T, cu_seqlens.numel() - 1, dev, host
 
 
+def _wanted(want_final, final_state_out):
+    if final_state_out is not None and not want_final:
+        raise ValueError("final_state_out needs output_final_state")
+
+
 def _no_outs(**outs):
     for name, t in outs.items():
         if t is not None:
@@ -327,6 +332,9 @@ def rms_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.Tenso
     dy = _cotangent("dy", dy, x, dev)
     if dresidual is not None:
         dresidual = _cotangent("dresidual", dresidual, x, dev)
+    if any(t is not None and _row_stride(t) is None for t in (x, gate)):
+        dy = dy.contiguous()
+        dresidual = dresidual if dresidual is None else dresidual.contiguous()
     heads, ((xp, xs), (dp, ds), (gp, gs), (rp, rs)) = _norm_rows((("x", x), ("dy", dy), ("gate", gate), ("dresidual", dresidual)), x, dev)
     dgate = dw = None
     if gate is not None:
@@ -357,6 +365,7 @@ def _causal_conv_fwd(x, conv_w, initial_state, want_final, cu_seqlens, cu_seqlen
     xp, xs = _act("x", x, x, dev)
     s0 = _state("initial_state", initial_state, (N, C, K), dev)
     y = _out("out", out, x, dev)
+    _wanted(want_final, final_state_out)
     fs = _out_as("final_state_out", final_state_out, (N, C, K), torch.float32, x.device, dev) if want_final else None
     _launch(call, call.pack(dt, B, T, C, K, xp, xs, conv_w.data_ptr(), s0, _ptr(fs), y.data_ptr(), _ptr(cu), _ptr(cu_host), N), dev)
     return y, fs, cu, cu_host
@@ -366,19 +375,18 @@ class _CausalConv(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, conv_w, initial_state, want_final, cu_seqlens, cu_seqlens_cpu):
         y, fs, cu, cu_host = _causal_conv_fwd(x, conv_w, initial_state, want_final, cu_seqlens, cu_seqlens_cpu)
-        ctx.save_for_backward(x, conv_w, initial_state)
-        ctx.cu = cu, cu_host
+        ctx.save_for_backward(x, conv_w, initial_state, cu, cu_host)
         ctx.set_materialize_grads(False)
         return y, fs
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dfs):
-        x, conv_w, s0 = ctx.saved_tensors
+        x, conv_w, s0, cu, cu_host = ctx.saved_tensors
         if dy is None:
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
         dx, dw, ds0 = causal_conv_bwd(
-            x, conv_w, dy, initial_state=s0, dfinal_state=dfs, cu_seqlens=ctx.cu[0], cu_seqlens_cpu=ctx.cu[1],
+            x, conv_w, dy, initial_state=s0, dfinal_state=dfs, cu_seqlens=cu, cu_seqlens_cpu=cu_host,
             want_dconv_w=ctx.needs_input_grad[1], want_dinitial_state=s0 is not None and ctx.needs_input_grad[2])
         return dx, dw, ds0, None, None, None
 
@@ -481,6 +489,7 @@ def _gated_scan_fwd(x, g, initial_state, want_final, sigmoid, lower_bound, cu_se
     gp, gs = _act("g", g, x, dev)
     s0 = _state("initial_state", initial_state, (N, D), dev)
     h = _out("out", out, x, dev)
+    _wanted(want_final, final_state_out)
     fs = _out_as("final_state_out", final_state_out, (N, D), torch.float32, x.device, dev) if want_final else None
     _launch_scratch(call, (dt, gate, B, T, D, xp, xs, gp, gs, h.data_ptr(), s0, _ptr(fs), _ptr(cu), _ptr(cu_host), N, has_lb, lb),
                     workspace, x.device, dev)
@@ -491,20 +500,20 @@ class _GatedScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, g, initial_state, want_final, sigmoid, lower_bound, cu_seqlens, cu_seqlens_cpu):
         h, fs, cu, cu_host = _gated_scan_fwd(x, g, initial_state, want_final, sigmoid, lower_bound, cu_seqlens, cu_seqlens_cpu)
-        ctx.save_for_backward(x if sigmoid else None, g, h, initial_state)
-        ctx.gate, ctx.cu = (sigmoid, lower_bound), (cu, cu_host)
+        ctx.save_for_backward(x if sigmoid else None, g, h, initial_state, cu, cu_host)
+        ctx.gate = sigmoid, lower_bound
         ctx.set_materialize_grads(False)
         return h, fs
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dh, dfs):
-        x, g, h, s0 = ctx.saved_tensors
+        x, g, h, s0, cu, cu_host = ctx.saved_tensors
         if dh is None:
             dh = torch.zeros(h.shape, dtype=h.dtype, device=h.device)
         dx, dg, ds0 = chunk_gated_scan_bwd(
             x, g, h, dh, initial_state=s0, dfinal_state=dfs, use_gate_sigmoid_in_kernel=ctx.gate[0],
-            lower_bound=ctx.gate[1], cu_seqlens=ctx.cu[0], cu_seqlens_cpu=ctx.cu[1],
+            lower_bound=ctx.gate[1], cu_seqlens=cu, cu_seqlens_cpu=cu_host,
             want_dinitial_state=s0 is not None and ctx.needs_input_grad[2])
         return dx, dg, ds0, None, None, None, None, None
 

@@ -262,6 +262,8 @@ def test_functions_refuse():
         lambda: kda.chunk_gated_scan(x, x, initial_state=torch.zeros(2, 16, device=DEV, dtype=torch.bfloat16)),
         lambda: kda.chunk_gated_scan_bwd(None, x, x, x, use_gate_sigmoid_in_kernel=True), lambda: kda.gated_scan_step(x, x, x),
         lambda: kda.gated_scan_step(x[:, 0], x[:, 0], None),
+        lambda: kda.causal_conv(x, cw, final_state_out=torch.empty(2, 16, 4, device=DEV)),
+        lambda: kda.chunk_gated_scan(x, x, final_state_out=torch.empty(2, 16, device=DEV)),
     ]
     for i, f in enumerate(bad):
         with pytest.raises(ValueError):
@@ -280,6 +282,43 @@ def test_functions_refuse():
               lambda: kda.rms_norm(draw(2, 20000))):
         with pytest.raises(KDAError):
             f()
+
+
+@pytest.mark.parametrize("cu", [[0, 700, 300, 900, 1000], [0, -5, 2000, 100, 1000], [1000, 900, 300, 100, 0], [7, 7, 7, 7, 7]], ids=str)
+@pytest.mark.parametrize("D", [40, 77, 40000])
+def test_offsets_that_are_not_what_the_host_was_told(cu, D):
+    """Offsets on the device may hold anything, whether the host's copy orders the work or
+    none: no access leaves the buffers, and calls that follow are as they were."""
+    import kimi_delta_attention_20_b200 as kda
+    T, N, K = 1000, 4, 4
+    host = torch.tensor([0, 240, 500, 760, 1000], dtype=torch.int32)
+    good, odd = host.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV)
+    x, g, w = draw(1, T, D, dtype=torch.bfloat16, seed=1), -draw(1, T, D, dtype=torch.bfloat16, seed=2).abs(), draw(D, K, seed=3)
+    s0, c0 = draw(N, D, seed=4), draw(N, D, K, seed=5)
+
+    def run(dev, cpu):
+        kw = dict(cu_seqlens=dev, cu_seqlens_cpu=cpu)
+        h, f = kda.chunk_gated_scan(x, g, initial_state=s0, output_final_state=True, **kw)
+        y, win = kda.causal_conv(x, w, initial_state=c0, output_final_state=True, **kw)
+        return (h, f, y, win, *kda.chunk_gated_scan_bwd(None, g, h, x, initial_state=s0, dfinal_state=s0, **kw),
+                *kda.causal_conv_bwd(x, w, x, initial_state=c0, dfinal_state=c0, **kw))
+
+    want = run(good, host)
+    run(odd, host)
+    run(odd, None)
+    torch.cuda.synchronize()
+    assert same(want, run(good, host))
+
+
+def test_offsets_changed_before_the_backward_are_noticed():
+    import kimi_delta_attention_20_b200 as kda
+    cu = torch.tensor([0, 3, 8], dtype=torch.int32, device=DEV)
+    x = draw(1, 8, 16, seed=1).requires_grad_()
+    for call in (lambda: kda.chunk_gated_scan(x, -x.detach().abs(), cu_seqlens=cu)[0], lambda: kda.causal_conv(x, draw(16, 4), cu_seqlens=cu)[0]):
+        y = call()
+        cu[1] = 4
+        with pytest.raises(RuntimeError):
+            y.sum().backward()
 
 
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")

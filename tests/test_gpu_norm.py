@@ -182,6 +182,31 @@ def test_norm_of_heads_in_a_fused_projection(dtype):
         kda.rms_norm(fused[..., :H * D].unflatten(-1, (H, D)).transpose(1, 2))
 
 
+def test_norm_autograd_of_heads_with_strided_cotangents():
+    """Heads of a fused projection whose norm is one part of a concatenation: autograd hands
+    back a slice whose heads do not lie back to back."""
+    import kimi_delta_attention_20_b200 as kda
+    B, T, H, D = 2, 5, 3, 24
+    fused, w = draw(B, T, 2 * H * D, dtype=torch.float32, seed=1).requires_grad_(), weights("f32", D, torch.float32, seed=2)
+    cot = draw(B, T, H, D + 9, dtype=torch.float32, seed=3)
+    x, g = (fused[..., k * H * D:(k + 1) * H * D].unflatten(-1, (H, D)) for k in range(2))
+    for kw in (dict(gate=g), dict(residual=g)):
+        fused.grad = None
+        r = kda.rms_norm(x, w, **kw)
+        y, s = (r, None) if "gate" in kw else r
+        loss = (torch.cat([y, torch.zeros(B, T, H, 9, device=DEV)], -1) * cot).sum()
+        if s is not None:
+            loss = loss + (torch.cat([torch.zeros(B, T, H, 9, device=DEV), s], -1) * cot).sum()
+        loss.backward()
+        dres = None if s is None else cot[..., 9:]
+        rx, rg, _, mag, _ = ref.norm_grads((x if s is None else s).detach(), cot[..., :D], w, kw.get("gate"), dres)
+        got = fused.grad.view(B, T, 2, H, D)
+        tol = rx.abs() * half(torch.float32) + mag * (54 * U + 2 * ref.norm_rel(D))
+        within("dx", got[:, :, 0], rx, tol)
+        if s is not None:
+            within("dresidual", got[:, :, 1], rx, tol)
+
+
 def test_norm_empty_and_large_offsets():
     import kimi_delta_attention_20_b200 as kda
     x = torch.empty(0, 64, device=DEV)

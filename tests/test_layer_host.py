@@ -191,6 +191,25 @@ def test_entry_points_refuse(fn, over, want):
     assert getattr(lib, fn)(None, None) == INVALID
 
 
+@pytest.mark.parametrize("fn,over", [
+    ("kda_causal_conv", dict(C=(1 << 28) + 1)), ("kda_causal_conv_bwd", dict(C=1 << 30)), ("kda_causal_conv_step", dict(C=(1 << 31) - 1)),
+    ("kda_gated_scan", dict(D=(1 << 28) + 1)), ("kda_gated_scan_bwd", dict(D=1 << 30)), ("kda_gated_scan_step", dict(D=(1 << 31) - 1)),
+])
+def test_entry_points_refuse_channels_beyond_their_range(fn, over):
+    assert getattr(_abi.load(), fn)(ctypes.byref(MAKE[fn](**over)), None) == INVALID
+
+
+@pytest.mark.parametrize("fn,over", [
+    ("kda_rms_norm_bwd", dict(workspace=A)), ("kda_rms_norm_bwd", dict(workspace=E)), ("kda_causal_conv_bwd", dict(workspace=B)),
+    ("kda_causal_conv_bwd", dict(workspace=D_ + 64)), ("kda_gated_scan", dict(T=4096, workspace=B, workspace_bytes=1 << 24)),
+    ("kda_gated_scan", dict(T=4096, workspace=C - 16, workspace_bytes=1 << 24)),
+    ("kda_gated_scan_bwd", dict(T=4096, workspace=B + 64, workspace_bytes=1 << 24)),
+    ("kda_gated_scan_bwd", dict(T=4096, workspace=E, workspace_bytes=1 << 24)),
+])
+def test_entry_points_refuse_a_workspace_over_a_tensor(fn, over):
+    assert getattr(_abi.load(), fn)(ctypes.byref(MAKE[fn](**over)), None) == INVALID
+
+
 @pytest.mark.parametrize("fn", ["kda_causal_conv", "kda_causal_conv_bwd", "kda_gated_scan", "kda_gated_scan_bwd"])
 @pytest.mark.parametrize("cu", [[1, 10], [0, 9], [0, 7, 5, 10]])
 def test_entry_points_refuse_bad_offsets(fn, cu):
