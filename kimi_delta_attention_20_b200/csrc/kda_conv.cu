@@ -80,10 +80,11 @@ __global__ void __launch_bounds__(32) conv_fwd_kernel(const __grid_constant__ Co
     const int lane = threadIdx.x, C = p.C, R = p.span.R, units = (C + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
     const int b = min(piece * p.piece, R), e = piece + 1 == p.pieces ? R : min(b + p.piece, R);
-    const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R)}, min(TC, C - c0) * (int)sizeof(T), lane};
+    RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R)}, min(TC, C - c0) * (int)sizeof(T), lane};
+    ring.begin(0, b);
 #pragma unroll 1
     for (int k = 0; k < ST - 1; ++k) {
-        if (b + k * S < e) ring.load(k, 0, b + k * S, b, e);
+        if (b + k * S < e) ring.template load<1>(k, 0, b + k * S, b, e);
         cp_async_commit();
     }
     float w[K][W];
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(32) conv_fwd_kernel(const __grid_constant__ Co
         cp_async_wait_group<ST - 2>();
         __syncwarp();
         const int ahead = r + (ST - 1) * S;
-        if (ahead < e) ring.load(next, 0, ahead, b, e);
+        if (ahead < e) ring.template load<1>(next, 0, ahead, b, e);
         cp_async_commit();
         // row r + s with the window's oldest input in slot j
         auto one = [&](int s, int j) {
@@ -164,11 +165,13 @@ __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ Co
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
     const int b = min(piece * p.piece, R), e = piece + 1 == p.pieces ? R : min(b + p.piece, R);
     const int stop = b < e ? min(e + K - 1, R) : e;  // rows that are walked
-    const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R), walk_tensor<T>(p.dy, p.dy_stride, c0, C, R)},
-                  min(TC, C - c0) * (int)sizeof(T), lane};
+    RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, C, R), walk_tensor<T>(p.dy, p.dy_stride, c0, C, R)},
+            min(TC, C - c0) * (int)sizeof(T), lane};
+    ring.begin(0, b);
+    ring.begin(1, b);
     auto load = [&](int at, int row) {
-        ring.load(at, 0, row, b, stop);
-        ring.load(at, 1, row, b, stop);
+        ring.template load<1>(at, 0, row, b, stop);
+        ring.template load<1>(at, 1, row, b, stop);
     };
 #pragma unroll 1
     for (int k = 0; k < ST - 1; ++k) {

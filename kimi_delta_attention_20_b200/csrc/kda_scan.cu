@@ -54,6 +54,23 @@ template <typename T, bool SIG> __device__ __forceinline__ void decay(float g, f
     }
 }
 
+// Of a lane's channels.
+template <typename T, bool SIG, int W> __device__ __forceinline__ void decays(const float (&g)[W], float lb, float (&a)[W], float (&b)[W]) {
+    if constexpr (!SIG && sizeof(T) == 2) {
+        float l[W];
+        vset(l, kLog2e);
+#pragma unroll
+        for (int i = 0; i < W; ++i) a[i] = max_nan(g[i], lb);
+        vmul(a, l, a);
+#pragma unroll
+        for (int i = 0; i < W; ++i) a[i] = ex2_fast(a[i]);
+        vset(b, 1.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) decay<T, SIG>(g[i], lb, a[i], b[i]);
+    }
+}
+
 // State n's channels, or zeros.
 template <int W> __device__ __forceinline__ void get_state(const float *states, int n, int c, int D, float (&v)[W]) {
 #pragma unroll
@@ -208,9 +225,43 @@ __device__ __forceinline__ void step_fwd(const R &ring, int slot, int s, int r, 
     float g[W], b[W];
     ring.get(slot, 0, s, r, v);
     ring.get(slot, 1, s, r, g);
-#pragma unroll
-    for (int i = 0; i < W; ++i) decay<T, SIG>(g[i], lb, a[i], b[i]);
+    decays<T, SIG>(g, lb, a, b);
     if (SIG) vmul(v, b, v);
+}
+
+// The same of rows s0 .. s0+UN-1 of a stage, one operation of all of them after the other: a
+// walker has its scheduler almost to itself, so neighbouring instructions have to be
+// independent (31744 x 12288: 502 us; 529 row after row).
+template <typename T, bool SIG, int UN, typename R, int W>
+__device__ __forceinline__ void steps_fwd(const R &ring, int slot, int s0, int r, float lb, float (&a)[UN][W], float (&v)[UN][W]) {
+    float b[UN][W];
+#pragma unroll
+    for (int s = 0; s < UN; ++s) ring.get(slot, 1, s0 + s, r + s, a[s]);
+#pragma unroll
+    for (int s = 0; s < UN; ++s) ring.get(slot, 0, s0 + s, r + s, v[s]);
+    if constexpr (!SIG && sizeof(T) == 2) {
+        float l[W];
+        vset(l, kLog2e);
+#pragma unroll
+        for (int s = 0; s < UN; ++s)
+#pragma unroll
+            for (int i = 0; i < W; ++i) a[s][i] = max_nan(a[s][i], lb);
+#pragma unroll
+        for (int s = 0; s < UN; ++s) vmul(a[s], l, a[s]);
+#pragma unroll
+        for (int s = 0; s < UN; ++s)
+#pragma unroll
+            for (int i = 0; i < W; ++i) a[s][i] = ex2_fast(a[s][i]);
+    } else {
+#pragma unroll
+        for (int s = 0; s < UN; ++s) {
+            float g[W];
+#pragma unroll
+            for (int i = 0; i < W; ++i) g[i] = a[s][i];
+            decays<T, SIG>(g, lb, a[s], b[s]);
+            if (SIG) vmul(v[s], b[s], v[s]);
+        }
+    }
 }
 
 template <typename T, int G, int LB, bool SIG>
@@ -222,11 +273,13 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
     int b, e;
     piece_rows(p.cut, p.span, piece, b, e);
-    const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, D, R), walk_tensor<T>(p.g, p.g_stride, c0, D, R)},
-                  min(TC, D - c0) * (int)sizeof(T), lane};
+    RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, D, R), walk_tensor<T>(p.g, p.g_stride, c0, D, R)},
+            min(TC, D - c0) * (int)sizeof(T), lane};
+    ring.begin(0, b);
+    ring.begin(1, b);
     auto load = [&](int slot, int row) {
-        ring.load(slot, 0, row, b, e);
-        ring.load(slot, 1, row, b, e);
+        ring.template load<1>(slot, 0, row, b, e);
+        ring.template load<1>(slot, 1, row, b, e);
     };
     if (b < e) {
 #pragma unroll 1
@@ -267,13 +320,13 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
         if (min(q.end, e) >= r + S) {
             auto rows = [&](int s0) {  // the decays of UN rows, then the rows
                 float a[UN][W], v[UN][W];
+                steps_fwd<T, SIG, UN>(ring, slot, s0, r + s0, p.lb, a, v);
 #pragma unroll
-                for (int s = 0; s < UN; ++s) step_fwd<T, SIG>(ring, slot, s0 + s, r + s0 + s, p.lb, a[s], v[s]);
+                for (int s = 0; s < UN; ++s) vfma(a[s], s ? v[s - 1] : h, v[s], v[s]);
 #pragma unroll
-                for (int s = 0; s < UN; ++s) {
-                    vfma(a[s], h, v[s], h);
-                    put_row<G>(out + (long long)(s0 + s) * D, c, D, lane, h);
-                }
+                for (int s = 0; s < UN; ++s) put_row<G>(out + (long long)(s0 + s) * D, c, D, lane, v[s]);
+#pragma unroll
+                for (int i = 0; i < W; ++i) h[i] = v[UN - 1][i];
             };
             if constexpr (UN == S) {
                 rows(0);
@@ -311,11 +364,13 @@ __global__ void __launch_bounds__(32) scan_reduce_kernel(const __grid_constant__
     if (q.end <= e) return;
     const bool begins = q.start >= b;
     b = max(b, q.start);
-    const RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, D, R), walk_tensor<T>(p.g, p.g_stride, c0, D, R)},
-                  min(TC, D - c0) * (int)sizeof(T), lane};
+    RN ring{dyn, {walk_tensor<T>(p.x, p.x_stride, c0, D, R), walk_tensor<T>(p.g, p.g_stride, c0, D, R)},
+            min(TC, D - c0) * (int)sizeof(T), lane};
+    ring.begin(0, b);
+    ring.begin(1, b);
     auto load = [&](int slot, int row) {
-        ring.load(slot, 0, row, b, e);
-        ring.load(slot, 1, row, b, e);
+        ring.template load<1>(slot, 0, row, b, e);
+        ring.template load<1>(slot, 1, row, b, e);
     };
 #pragma unroll 1
     for (int k = 0; k < ST - 1; ++k) {
@@ -390,12 +445,16 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
     RN ring{dyn, {walk_tensor<T>(p.g, p.g_stride, c0, D, R), walk_tensor<T>(p.dout, p.dout_stride, c0, D, R),
                   walk_tensor<T>(p.h, p.h_stride, c0, D, R)}, min(TC, D - c0) * (int)sizeof(T), lane};
     if (SIG) ring.t[N - 1] = walk_tensor<T>(p.x, p.x_stride, c0, D, R);
+    ring.begin(0, e - S);
+    ring.begin(1, e - S);
+    ring.begin(2, e - S - 1);
+    if (SIG) ring.begin(N - 1, e - S);
     // a stage's rows from `row` on, of h the rows before them
     auto load = [&](int slot, int row) {
-        ring.load(slot, 0, row, b, e);
-        ring.load(slot, 1, row, b, e);
-        ring.load(slot, 2, row - 1, max(b - 1, 0), e - 1);
-        if (SIG) ring.load(slot, N - 1, row, b, e);
+        ring.template load<-1>(slot, 0, row, b, e);
+        ring.template load<-1>(slot, 1, row, b, e);
+        ring.template load<-1>(slot, 2, row - 1, max(b - 1, 0), e - 1);
+        if (SIG) ring.template load<-1>(slot, N - 1, row, b, e);
     };
     if (b < e) {
 #pragma unroll 1
@@ -426,8 +485,7 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
             if (first) get_state(p.s0, q.n, c, D, hp);
             else ring.get(slot, 2, s, row - 1, hp);
             if (SIG) ring.get(slot, N - 1, s, row, x);
-#pragma unroll
-            for (int i = 0; i < W; ++i) decay<T, SIG>(g[i], p.lb, a[i], w[i]);
+            decays<T, SIG>(g, p.lb, a, w);
             vadd(d, k, d);
             vmul(a, d, k);
             if (SIG) {
@@ -482,11 +540,13 @@ __global__ void __launch_bounds__(32) scan_reduce_bwd_kernel(const __grid_consta
     if (q.start >= b) return;
     const bool ends = q.end <= e;
     e = min(e, q.end);
-    const RN ring{dyn, {walk_tensor<T>(p.g, p.g_stride, c0, D, R), walk_tensor<T>(p.dout, p.dout_stride, c0, D, R)},
-                  min(TC, D - c0) * (int)sizeof(T), lane};
+    RN ring{dyn, {walk_tensor<T>(p.g, p.g_stride, c0, D, R), walk_tensor<T>(p.dout, p.dout_stride, c0, D, R)},
+            min(TC, D - c0) * (int)sizeof(T), lane};
+    ring.begin(0, e - S);
+    ring.begin(1, e - S);
     auto load = [&](int slot, int row) {
-        ring.load(slot, 0, row, b, e);
-        ring.load(slot, 1, row, b, e);
+        ring.template load<-1>(slot, 0, row, b, e);
+        ring.template load<-1>(slot, 1, row, b, e);
     };
 #pragma unroll 1
     for (int k = 0; k < ST - 1; ++k) {
@@ -509,8 +569,7 @@ __global__ void __launch_bounds__(32) scan_reduce_bwd_kernel(const __grid_consta
             float g[W], d[W], a[W], w[W];
             ring.get(slot, 0, s, r + s, g);
             ring.get(slot, 1, s, r + s, d);
-#pragma unroll
-            for (int i = 0; i < W; ++i) decay<T, SIG>(g[i], p.lb, a[i], w[i]);
+            decays<T, SIG>(g, p.lb, a, w);
             vadd(d, h, d);
             vmul(a, d, h);
             vmul(A, a, A);

@@ -169,22 +169,35 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
     WalkTensor t[N];
     int width;  // bytes of a row that are the walker's
     int lane;
+    const char *src[N];  // where the lane's next copies begin
+
+    // A lane's first copy of a stage: its row in the stage, its byte in the row.
+    static constexpr int PER = ROW / G;  // copies of a row
+    static constexpr int ROWS = PER < 32 ? 32 / PER : 1, ROUNDS = PER < 32 ? 1 : PER / 32;
+    static_assert(!WHOLE || S % ROWS == 0, "whole rounds");
+    __device__ __forceinline__ int lane_row() const { return PER < 32 ? lane / PER : 0; }
+    __device__ __forceinline__ int lane_byte() const { return (PER < 32 ? lane % PER : lane) * G; }
+
+    // The next stage of tensor i to be loaded is the one that begins at `row`.
+    __device__ __forceinline__ void begin(int i, int row) {
+        src[i] = t[i].at + (long long)row * t[i].stride;
+        if (WHOLE) src[i] += lane_row() * t[i].stride + lane_byte();
+    }
 
     template <int B> static __device__ __forceinline__ void copy(unsigned to, const char *from) {
         if constexpr (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
         else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(B) : "memory");
     }
 
-    // Starts the copies of rows row .. row+S-1 of tensor i into stage `slot`: those in [lo, hi).
-    __device__ __forceinline__ void load(int slot, int i, int row, int lo, int hi) const {
+    // Starts the copies of the next stage of tensor i, rows row .. row+S-1, into `slot`: those
+    // in [lo, hi). DIR: whether the stage after it lies behind (1) or before it (-1).
+    template <int DIR> __device__ __forceinline__ void load(int slot, int i, int row, int lo, int hi) {
+        const char *from = src[i];
+        src[i] += DIR * S * t[i].stride;
         char *to = base + (slot * N + i) * PART;
         const bool inner = row >= lo && row + S <= hi;
         if constexpr (WHOLE) {
-            constexpr int PER = ROW / G;  // copies of a row
-            constexpr int ROWS = PER < 32 ? 32 / PER : 1, ROUNDS = PER < 32 ? 1 : PER / 32;
-            static_assert(S % ROWS == 0, "whole rounds");
-            const int lr = PER < 32 ? lane / PER : 0, lc = (PER < 32 ? lane % PER : lane) * G;
-            const char *src = t[i].at + (long long)(row + lr) * t[i].stride + lc;
+            const int lr = lane_row(), lc = lane_byte();
             const unsigned d = (unsigned)__cvta_generic_to_shared(to + lr * PITCH + lc);
             const long long step = ROWS * t[i].stride;
             // Unrolled for a partly filled unit too where copies are narrow and many (131072 x 257
@@ -193,30 +206,29 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
             constexpr bool MASKED = G <= 4;
             if (inner && (MASKED || width == ROW)) {
 #pragma unroll
-                for (int k = 0; k < S; k += ROWS, src += step)
+                for (int k = 0; k < S; k += ROWS, from += step)
 #pragma unroll
                     for (int j = 0; j < ROUNDS; ++j)
-                        if (!MASKED || lc + j * 32 * G < width) copy<G>(d + k * PITCH + j * 32 * G, src + j * 32 * G);
+                        if (!MASKED || lc + j * 32 * G < width) copy<G>(d + k * PITCH + j * 32 * G, from + j * 32 * G);
                 return;
             }
 #pragma unroll 1
-            for (int k = 0; k < S; k += ROWS, src += step) {
+            for (int k = 0; k < S; k += ROWS, from += step) {
                 const int r = row + lr + k;
                 if (r >= lo && r < hi)
 #pragma unroll
                     for (int j = 0; j < ROUNDS; ++j)
-                        if (lc + j * 32 * G < width) copy<G>(d + k * PITCH + j * 32 * G, src + j * 32 * G);
+                        if (lc + j * 32 * G < width) copy<G>(d + k * PITCH + j * 32 * G, from + j * 32 * G);
             }
         } else {
             constexpr int WORDS = PITCH / 16, COUNT = S * WORDS;
             // words near the tensor's first and last rows may reach beyond it
-            const char *from = t[i].at + (long long)row * t[i].stride;
             const bool plain = inner && from - 14 >= t[i].begin && from + (S - 1) * t[i].stride + width + 14 <= t[i].end;
             if (plain) {
 #pragma unroll
                 for (int q = 0; q < (COUNT + 31) / 32; ++q) {
                     const int x = q * 32 + lane, k = x / WORDS, j = x - k * WORDS;
-                    const char *a = t[i].at + (long long)(row + k) * t[i].stride;
+                    const char *a = from + k * t[i].stride;
                     const int off = (int)((uint32_t)reinterpret_cast<uintptr_t>(a) & 15u);
                     if (x < COUNT && 16 * j - off < width) copy<16>((unsigned)__cvta_generic_to_shared(to + x * 16), a - off + 16 * j);
                 }
@@ -226,7 +238,7 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
             for (int x = lane; x < COUNT; x += 32) {
                 const int k = x / WORDS, j = x - k * WORDS, r = row + k;
                 if (r < lo || r >= hi) continue;
-                const char *a = t[i].at + (long long)r * t[i].stride;
+                const char *a = from + k * t[i].stride;
                 const int off = (int)((uint32_t)reinterpret_cast<uintptr_t>(a) & 15u);
                 const char *w = a - off + 16 * j;
                 if (16 * j - off >= width) continue;
