@@ -162,6 +162,7 @@ template <typename T, int G, int K>
 __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p) {
     using RN = BwdRing<T, G>;
     constexpr int W = RN::W, S = kStage, ST = kBwdStages, TC = walk_channels<T, kLB>();
+    let_next_pass_start();
     extern __shared__ __align__(16) char dyn[];
     const int lane = threadIdx.x, C = p.C, R = p.span.R, units = (C + TC - 1) / TC;
     const int piece = blockIdx.x / units, c0 = (blockIdx.x - piece * units) * TC, c = c0 + lane * W;
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(32) conv_bwd_kernel(const __grid_constant__ Co
 // dw[c, k]: the sum of its slices [K, C].
 __global__ void __launch_bounds__(1024) conv_dw_kernel(const float *partial, float *dw, int slices, int C, int K) {
     const long long cols = (long long)K * C, col = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
+    wait_for_last_pass();
     const float v = slice_sum(partial, slices, cols, col);
     if (threadIdx.x < 32 && col < cols) dw[col % C * K + col / C] = v;
 }
@@ -372,9 +374,7 @@ template <typename T, int G, int K> cudaError_t run_fwd(const ConvParams &p, cud
 template <typename T, int G, int K> cudaError_t run_bwd(const ConvBwdParams &p, cudaStream_t st) {
     const cudaError_t e = run_walk<T>(conv_bwd_kernel<T, G, K>, p, BwdRing<T, G>::BYTES, st);
     if (e != cudaSuccess || !p.dw) return e;
-    count_launch();
-    conv_dw_kernel<<<(unsigned)(((long long)p.C * K + 31) / 32), 1024, 0, st>>>(p.partial, p.dw, p.pieces, p.C, K);
-    return cudaGetLastError();
+    return launch_next_pass(conv_dw_kernel, (unsigned)(((long long)p.C * K + 31) / 32), 1024, st, (const float *)p.partial, p.dw, p.pieces, p.C, K);
 }
 template <typename T, int K> cudaError_t run_step(const ConvStepParams &p, cudaStream_t st) {
     const long long n = (long long)p.N * p.C;

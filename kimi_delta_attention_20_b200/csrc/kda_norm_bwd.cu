@@ -10,6 +10,7 @@ namespace {
 template <typename T, int G, int TPR, int NU, bool GATE>
 __global__ void __launch_bounds__(norm_threads<TPR>(), norm_resident(true, TPR, NU)) norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
     constexpr int NT = norm_threads<TPR>(), ROWS = NT / TPR, P = access_channels<T, G>(), NA = 8 * NU / P;
+    let_next_pass_start();
     __shared__ float red[2][2][norm_red<TPR>()];
     __shared__ float slice[ROWS > 1 ? ROWS * TPR * 8 * NU : 1];
     const int t = threadIdx.x % TPR, lr = threadIdx.x / TPR, D = p.D;
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), norm_resident(true, TPR, 
 // dw: the sum of its slices.
 template <typename T> __global__ void __launch_bounds__(1024) norm_dw_kernel(const float *partial, void *dw, int f32, int slices, int D) {
     const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+    wait_for_last_pass();
     const float v = slice_sum(partial, slices, D, c);
     if (threadIdx.x >= 32 || c >= D) return;
     if (f32) static_cast<float *>(dw)[c] = v;
@@ -115,9 +117,7 @@ template <typename T, int G, int TPR, int NU> struct Bwd {
         else norm_bwd_kernel<T, G, TPR, NU, false><<<ctas, norm_threads<TPR>(), 0, st>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || !p.dweight) return e;
-        count_launch();
-        norm_dw_kernel<T><<<(p.D + 31) / 32, 1024, 0, st>>>(p.partial, p.dweight, p.weight_f32, ctas, p.D);
-        return cudaGetLastError();
+        return launch_next_pass(norm_dw_kernel<T>, (p.D + 31) / 32, 1024, st, (const float *)p.partial, p.dweight, p.weight_f32, ctas, p.D);
     }
 };
 

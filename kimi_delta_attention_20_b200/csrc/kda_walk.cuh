@@ -7,6 +7,8 @@
 // between them.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_common.cuh"
 #include "kda_stage.cuh"
 
@@ -22,6 +24,31 @@ struct RowSpan {
 // Channels of a lane, and of a walker.
 template <typename T, int LB> constexpr int lane_channels() { return LB / (int)sizeof(T); }
 template <typename T, int LB> constexpr int walk_channels() { return 32 * lane_channels<T, LB>(); }
+
+// ---------------------------------------------------------------- passes of a call
+// The pass that joins a backward pass's partial sums is queued while that one runs: its CTAs
+// come up as SMs empty and wait for the sums, all of them, so that its end is the end of both
+// (1 us a call). The scan's passes follow one another plainly: a walk whose CTAs come up
+// early crowds the first SMs to empty (131072 x 257: 244 us against 211).
+__device__ __forceinline__ void let_next_pass_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_last_pass() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P>
+cudaError_t launch_next_pass(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t st,
+                        typename std::common_type<P>::type... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(threads);
+    c.stream = st;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    count_launch();
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args...);
+    return e != cudaSuccess ? cudaGetLastError() : e;
+}
 
 // ---------------------------------------------------------------- arithmetic
 // The SFU's exponential (off by 2 steps) and reciprocal (1 step), for bf16 results.
