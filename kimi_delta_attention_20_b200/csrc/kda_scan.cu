@@ -698,10 +698,11 @@ void lay_out(ScanCut *c, int D, bool bf16, void *workspace) {
 
 // Lanes of 8 bytes take about two thirds of the instructions an element; lanes of 4 make
 // twice the walkers, and are taken where they save the cut along time (31744 x 12288 packed
-// of four sequences: 500 us in one pass, against 637 with lanes of 8 in two).
+// of four sequences: 511 us in one pass, 637 with lanes of 8 in two; x 12292, by 8 bytes: 859
+// against 996), but for accesses of less than 8 bytes (x 12289: 2017 against 1021).
 ScanCut scan_cut(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int g) {
     const ScanCut wide = cut_for(sp, cu_host, D, bf16, 8);
-    if (!wide.carries || g < 16) return wide;
+    if (!wide.carries || g < 8) return wide;
     const ScanCut narrow = cut_for(sp, cu_host, D, bf16, 4);
     return narrow.carries ? wide : narrow;
 }
@@ -723,27 +724,31 @@ template <int W> cudaError_t run_carry(const ScanCut &c, int D, bool bf16, int b
     return cudaGetLastError();
 }
 
+// Lanes of 4 bytes come with one pass over the rows and wide accesses (see scan_cut).
 template <typename T, int G, int LB, bool SIG> cudaError_t run_fwd_lb(const ScanParams &p, cudaStream_t st) {
     constexpr int ring = ScanRing<T, G, LB, 2>::BYTES;
     cudaError_t e = cudaSuccess;
-    if (p.cut.carries) e = run_walk<T>(scan_reduce_kernel<T, G, LB, SIG>, p, ring, st);
-    if (e == cudaSuccess) e = run_carry<lane_channels<T, LB>()>(p.cut, p.D, sizeof(T) == 2, 0, st);
+    if constexpr (LB == 8) {
+        if (p.cut.carries) e = run_walk<T>(scan_reduce_kernel<T, G, LB, SIG>, p, ring, st);
+        if (e == cudaSuccess) e = run_carry<lane_channels<T, LB>()>(p.cut, p.D, sizeof(T) == 2, 0, st);
+    }
     return e != cudaSuccess ? e : run_walk<T>(scan_fwd_kernel<T, G, LB, SIG>, p, ring, st);
 }
 template <typename T, int G, int LB, bool SIG> cudaError_t run_bwd_lb(const ScanBwdParams &p, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    if (p.cut.carries) e = run_walk<T>(scan_reduce_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, 2>::BYTES, st);
-    if (e == cudaSuccess) e = run_carry<lane_channels<T, LB>()>(p.cut, p.D, sizeof(T) == 2, 1, st);
+    if constexpr (LB == 8) {
+        if (p.cut.carries) e = run_walk<T>(scan_reduce_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, 2>::BYTES, st);
+        if (e == cudaSuccess) e = run_carry<lane_channels<T, LB>()>(p.cut, p.D, sizeof(T) == 2, 1, st);
+    }
     return e != cudaSuccess ? e : run_walk<T>(scan_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, SIG ? 4 : 3>::BYTES, st);
 }
-// Lanes of 4 bytes come with 16-byte accesses only (see scan_cut).
 template <typename T, int G, bool SIG> cudaError_t run_fwd(const ScanParams &p, cudaStream_t st) {
-    if constexpr (G == 16)
+    if constexpr (G >= 8)
         if (p.cut.lb == 4) return run_fwd_lb<T, G, 4, SIG>(p, st);
     return run_fwd_lb<T, G, 8, SIG>(p, st);
 }
 template <typename T, int G, bool SIG> cudaError_t run_bwd(const ScanBwdParams &p, cudaStream_t st) {
-    if constexpr (G == 16)
+    if constexpr (G >= 8)
         if (p.cut.lb == 4) return run_bwd_lb<T, G, 4, SIG>(p, st);
     return run_bwd_lb<T, G, 8, SIG>(p, st);
 }

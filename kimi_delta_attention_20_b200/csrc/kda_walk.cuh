@@ -204,11 +204,18 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
     static_assert(!WHOLE || S % ROWS == 0, "whole rounds");
     __device__ __forceinline__ int lane_row() const { return PER < 32 ? lane / PER : 0; }
     __device__ __forceinline__ int lane_byte() const { return (PER < 32 ? lane % PER : lane) * G; }
+    // Where it reads from. In the last, partly filled unit lanes beyond the row copy its first
+    // bytes, to places that nothing is written from: predicates on every copy instead cost
+    // 31744 x 12288 bf16 537 us against 511, a loop over rows 8192 x 2000 backward 58 against 49.
+    // Rows of two narrow copies a lane (MASKED) do take predicates: 131072 x 257 fp32 211 us,
+    // where copying the first bytes 64 times over takes 457.
+    static constexpr bool MASKED = ROUNDS > 1;
+    __device__ __forceinline__ int lane_from() const { return MASKED || lane_byte() < width ? lane_byte() : 0; }
 
     // The next stage of tensor i to be loaded is the one that begins at `row`.
     __device__ __forceinline__ void begin(int i, int row) {
         src[i] = t[i].at + (long long)row * t[i].stride;
-        if (WHOLE) src[i] += lane_row() * t[i].stride + lane_byte();
+        if (WHOLE) src[i] += lane_row() * t[i].stride + lane_from();
     }
 
     template <int B> static __device__ __forceinline__ void copy(unsigned to, const char *from) {
@@ -227,11 +234,7 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
             const int lr = lane_row(), lc = lane_byte();
             const unsigned d = (unsigned)__cvta_generic_to_shared(to + lr * PITCH + lc);
             const long long step = ROWS * t[i].stride;
-            // Unrolled for a partly filled unit too where copies are narrow and many (131072 x 257
-            // fp32 scanned: 209 us, 258 without); wide ones go without predicates there (31744 x
-            // 12288 bf16: 497 us, 537 with).
-            constexpr bool MASKED = G <= 4;
-            if (inner && (MASKED || width == ROW)) {
+            if (inner) {
 #pragma unroll
                 for (int k = 0; k < S; k += ROWS, from += step)
 #pragma unroll
@@ -245,7 +248,7 @@ template <typename T, int G, int LB, int S, int N, int STAGES> struct Ring {
                 if (r >= lo && r < hi)
 #pragma unroll
                     for (int j = 0; j < ROUNDS; ++j)
-                        if (lc + j * 32 * G < width) copy<G>(d + k * PITCH + j * 32 * G, from + j * 32 * G);
+                        if (!MASKED || lc + j * 32 * G < width) copy<G>(d + k * PITCH + j * 32 * G, from + j * 32 * G);
             }
         } else {
             constexpr int WORDS = PITCH / 16, COUNT = S * WORDS;

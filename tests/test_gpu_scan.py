@@ -77,7 +77,8 @@ def test_scan_batch(N, T, form, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("lens,D", [([5000], 4), ([4700, 0, 300], 130), ([2500], 1000), ([700], 2600), ([300, 40], 20000), ([150], 39000),
-                                    ([300, 200, 100, 257], 8448), ([300, 200, 100, 257], 17024)])
+                                    ([300, 200, 100, 257], 8448), ([300, 200, 100, 257], 17024),
+                                    ([300, 200, 100, 257], 8450), ([300, 200, 100, 257], 8452)])
 def test_scan_cut_along_time(lens, D, dtype):
     """Sequences cut into many pieces, few, or none, with lanes of 8 and of 4 bytes."""
     check_scan(lens, D, dtype, FORMS[0], seed=D)
