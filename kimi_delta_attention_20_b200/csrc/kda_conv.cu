@@ -7,7 +7,7 @@
 //
 // 4 bytes an element forward, 6 backward (bf16), but bound by the special-function unit, which
 // takes two instructions an element and is 61 % busy, and in the backward by issue: 8192 x 6144
-// in 41 us (4.9 TB/s), 65536 x 1024 backward in 87 us (4.7 TB/s). A walker slides the window
+// in 41 us (4.9 TB/s), 65536 x 1024 backward in 85 us (4.7 TB/s). A walker slides the window
 // down its piece of the rows in registers. Nothing is carried between pieces but K - 1
 // rows that are read twice, so pieces are cut for full waves of walkers: sixteen an SM with
 // rings of 12 KiB, since they need the arithmetic of many warps beside the bytes in flight
