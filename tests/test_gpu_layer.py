@@ -321,6 +321,27 @@ def test_offsets_changed_before_the_backward_are_noticed():
             y.sum().backward()
 
 
+def test_elements_beyond_32_bits():
+    """The last rows of tensors of over 2^31 elements, behind rows of zeros, are those of a
+    call of these rows alone."""
+    import kimi_delta_attention_20_b200 as kda
+    T, C, K, n = 65600, 32776, 4, 5
+    w, tail = draw(C, K, seed=1), draw(1, n, C, dtype=torch.bfloat16, seed=2)
+    tail_g, tail_d = -draw(1, n, C, dtype=torch.bfloat16, seed=3).abs(), draw(1, n, C, dtype=torch.bfloat16, seed=4)
+    x, g, d = (torch.zeros(1, T, C, dtype=torch.bfloat16, device=DEV) for _ in range(3))
+    x[:, -n:], g[:, -n:], d[:, -n:] = tail, tail_g, tail_d
+
+    def run(x, g, d):
+        h, _ = kda.chunk_gated_scan(x, g)
+        outs = [h, kda.causal_conv(x, w)[0], *kda.chunk_gated_scan_bwd(None, g, h, d)[:2], kda.causal_conv_bwd(x, w, d, want_dconv_w=False)[0]]
+        first = [t[:, :-n].abs().max().item() for t in outs] if x.shape[1] > n else []
+        return [t[:, -n:].clone() for t in outs], first
+
+    want, _ = run(tail, tail_g, tail_d)
+    got, first = run(x, g, d)
+    assert same(want, got) and first[:2] == [0.0, 0.0]
+
+
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
 def test_on_another_device():
     p = call_params(60)

@@ -85,6 +85,14 @@ def test_scan_cut_along_time(lens, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("form", [FORMS[0], FORMS[2]], ids=str)
+@pytest.mark.parametrize("lens,D", [([20000], 4), ([9000, 0, 1, 8063, 64, 3000], 41)], ids=str)
+def test_scan_cut_into_many_pieces(lens, D, form, dtype):
+    """More pieces than a walker composes the maps of itself."""
+    check_scan(lens, D, dtype, form, seed=D)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N,T,D", [(1, 3000, 20), (3, 500, 260), (4, 300, 8448), (1000, 2, 64), (300, 7, 1024)])
 def test_scan_cut_of_a_batch(N, T, D, dtype):
     check_scan([T] * N, D, dtype, FORMS[2], seed=N + T, span={})
