@@ -91,8 +91,8 @@ template <int W> __device__ __forceinline__ void put_state(float *states, int n,
 __device__ __forceinline__ void piece_rows(const ScanCut &cut, const RowSpan &sp, int piece, int &b, int &e) {
     if (cut.kind == kCutBatch) {
         const int n = piece / cut.per, j = piece - n * cut.per;
-        b = n * sp.T + min(j * cut.rows, sp.T);
-        e = n * sp.T + min((j + 1) * cut.rows, sp.T);
+        b = n * sp.T + j * cut.rows;
+        e = n * sp.T + (j + 1 == cut.per ? sp.T : (j + 1) * cut.rows);  // the last piece's rows may end beyond 32 bits
     } else if (cut.kind == kCutSeqs) {
         b = min(max(sp.cu[piece], 0), sp.R);
         e = min(max(sp.cu[piece + 1], b), sp.R);
@@ -636,6 +636,9 @@ int units_of(int D, bool bf16, int lb) {
     return (D + tc - 1) / tc;
 }
 
+// Pieces of `each` rows; rows + each may pass 32 bits.
+int pieces_of(int rows, int each) { return (int)(((long long)rows + each - 1) / each); }
+
 // How the rows are cut for walkers of `lb` bytes a lane. Whole sequences where walkers of
 // whole sequences come to half of those that can run at a time, none more than three times
 // as long as the average (one pass; without the lengths on the host a packed batch is taken
@@ -663,7 +666,7 @@ ScanCut cut_for(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int
         const int per = (int)(want / sp.N);
         c.kind = kCutBatch;
         c.rows = stages(sp.T / per > kMinPiece ? (sp.T + per - 1) / per : kMinPiece);
-        c.per = (sp.T + c.rows - 1) / c.rows;
+        c.per = pieces_of(sp.T, c.rows);
         c.pieces = sp.N * c.per;
         c.carries = c.per > 1;
         return c;
@@ -678,7 +681,7 @@ ScanCut cut_for(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int
     }
     c.kind = kCutRows;
     c.rows = stages(sp.R / want > kMinPiece ? (sp.R + want - 1) / want : kMinPiece);
-    c.pieces = (sp.R + c.rows - 1) / c.rows;
+    c.pieces = pieces_of(sp.R, c.rows);
     c.carries = c.pieces > 1;
     return c;
 }
