@@ -401,8 +401,8 @@ typedef struct {
     const void *weight;       /* [D], NULL = ones */
     float eps;                /* >= 0 */
     void *y;                  /* [rows, D] out */
-    void *residual_out;       /* [rows, D] out, NULL when not wanted; may be `residual` or `x`
-                               * itself (same rows) */
+    void *residual_out;       /* [rows, D] out, NULL when not wanted or without a residual; may
+                               * be `residual` or `x` itself (same rows) */
     float *scales;            /* [rows, ceil(D / group_size)] out: 8-bit output; NULL: y has dtype */
     int group_size;           /* channels per scale: 32, 64 or 128, 0 = the whole row */
     int pow2_scales;

@@ -153,6 +153,7 @@ kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
     if (s != KDA_OK) return s;
     if (a->group_size != 0 && a->group_size != 32 && a->group_size != 64 && a->group_size != 128) return KDA_ERR_UNSUPPORTED;
     if (a->residual && a->gate) return KDA_ERR_UNSUPPORTED;
+    if (a->residual_out && !a->residual) return KDA_ERR_INVALID_ARGUMENT;
     if (a->rows == 0) return KDA_OK;
     const size_t esz = size_of(a->dtype);
     kda::NormParams p{};
@@ -177,7 +178,6 @@ kda_status kda_rms_norm(const kda_rms_norm_args *a, void *stream) {
             } else if ((c.in[i].hi - c.in[i].lo) != (uintptr_t)a->rows * a->D * esz) {
                 return KDA_ERR_INVALID_ARGUMENT;
             }
-        if (a->gate == a->residual_out) return KDA_ERR_INVALID_ARGUMENT;
     } else {
         c.output(a->residual_out, false, a->rows, a->D, esz);
     }
