@@ -380,9 +380,9 @@ KDA_API kda_status kda_chunk_fwd_noalloc_status(const kda_chunk_args *args, void
  *
  * With `scales`, y is 8-bit e4m3 (one byte an element) for an 8-bit product: each
  * row's channels in groups of group_size have scale = max(max|y| / 448, 2^-100) --
- * with pow2_scales the next power of two -- and hold the nearest e4m3 of y / scale
- * (a group of zeros has scale 2^-100 and zeros; a NaN in a group makes its scale
- * NaN).
+ * with pow2_scales the next power of two -- and hold the nearest e4m3 (ties to even)
+ * of the fp32 quotient y / scale, y in fp32 (a group of zeros has scale 2^-100 and
+ * zeros; a NaN in a group makes its scale NaN).
  */
 typedef struct {
     kda_dtype dtype;          /* of x, residual, gate, residual_out, and y without scales */

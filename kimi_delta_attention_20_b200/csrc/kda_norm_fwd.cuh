@@ -114,10 +114,16 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), norm_resident(false, TPR,
 #pragma unroll
                 for (int q = 0; q < NA; ++q) {
                     const int c = (q * TPR + t) * P;
-                    const float scale = group_scale(top[q], p.pow2), to = 1.f / scale;
+                    // s / scale as a division would round it: the product with the reciprocal is up to two
+                    // steps off, which would show next to a border of e4m3, and its remainder says by how
+                    // much. An infinite scale leaves no remainder to take: 0, or NaN of an infinity.
+                    const float scale = group_scale(top[q], p.pow2), to = 1.f / scale, by = scale < INFINITY ? scale : 0.f;
                     float v[P];
 #pragma unroll
-                    for (int i = 0; i < P; ++i) v[i] = s[q * P + i] * to;
+                    for (int i = 0; i < P; ++i) {
+                        v[i] = s[q * P + i] * to;
+                        v[i] = fmaf(fmaf(-v[i], by, s[q * P + i]), to, v[i]);
+                    }
                     store_e4m3<P, G == 16>(static_cast<uint8_t *>(p.y) + row * D, c, D, v);
                     if (whole ? c == 0 : c < D && c % p.group == 0) p.scales[row * groups + (whole ? 0 : c / p.group)] = scale;
                 }
