@@ -39,10 +39,21 @@ constexpr int ring_stages(int lb, int tensors) { return 96 / lb / tensors; }
 template <int G> constexpr int unrolled() { return G > 2 ? kStage : 2; }
 template <typename T, int G, int LB, int N> using ScanRing = Ring<T, G, LB, kStage, N, ring_stages(LB, N)>;
 
+// exp(g) of log-decays that are bf16, on the SFU, whose exponential is that of 2: log2 e is split
+// (Cody and Waite) into a head of 16 bits, whose product with the 8 bits of g is exact, and a
+// rest, whose factor is 1 + g rest ln 2 but for its square. That is off by 7 2^-24 of a at most:
+// 4 by the exponential, 1 by the last rounding, and (g rest ln 2)^2 / 2 < 1.6 where a is a
+// normal number. One product with log2 e would add 2 |g| of them, the same way at every
+// step of a constant gate. A lower bound of more than 8 bits rounds the product: |bound| more.
+constexpr float kLog2eHead = 47274.f / 32768.f;
+constexpr float kLog2eRest = (float)((1.4426950408889634 - 47274. / 32768.) * 0.6931471805599453);
+// Below it a is 0; and 0 (1 + g rest ln 2) stays 0 for g = -inf.
+constexpr float kNoDecayLeft = -150.f;
+
 // a of the gate input, and the weight b of x in the sigmoid form: 1 - a without the
 // cancellation, since a is close to 1 where memories are long. lb is -inf without a bound.
-// bf16 inputs take the SFU's exponential, which is off by 2 steps where a is near 1 and by
-// (4 + 2 |g|) 2^-24 of a in general; fp32 inputs take expf.
+// bf16 inputs take the SFU's exponential (in the sigmoid form of a rounded product, off by
+// (4 + 2 |g|) 2^-24 of the smaller of a and 1 - a); fp32 inputs take expf.
 template <typename T, bool SIG> __device__ __forceinline__ void decay(float g, float lb, float &a, float &b) {
     constexpr bool FAST = sizeof(T) == 2;
     if (SIG) {
@@ -50,28 +61,56 @@ template <typename T, bool SIG> __device__ __forceinline__ void decay(float g, f
         const float r = FAST ? rcp_fast(1.f + e) : 1.f / (1.f + e), q = e * r;
         a = g >= 0.f ? r : q;
         b = g >= 0.f ? q : r;
+    } else if (FAST) {
+        g = max_nan(g, fmaxf(lb, kNoDecayLeft));
+        a = ex2_fast(g * kLog2eHead);
+        a = fmaf(a, g * kLog2eRest, a);
+        b = 1.f;
     } else {
-        g = max_nan(g, lb);
-        a = FAST ? ex2_fast(g * kLog2e) : expf(g);
+        a = expf(max_nan(g, lb));
         b = 1.f;
     }
 }
 
-// Of a lane's channels.
-template <typename T, bool SIG, int W> __device__ __forceinline__ void decays(const float (&g)[W], float lb, float (&a)[W], float (&b)[W]) {
+// Of a lane's channels in N rows: g becomes a, one operation of all of them after the other
+// where the operations are few (see steps_fwd).
+template <typename T, bool SIG, int N, int W>
+__device__ __forceinline__ void decays(float (&a)[N][W], float lb, float (&b)[N][W]) {
     if constexpr (!SIG && sizeof(T) == 2) {
-        float l[W];
-        vset(l, kLog2e);
+        float head[W], rest[W], f[N][W];
+        vset(head, kLog2eHead);
+        vset(rest, kLog2eRest);
+        const float least = fmaxf(lb, kNoDecayLeft);
 #pragma unroll
-        for (int i = 0; i < W; ++i) a[i] = max_nan(g[i], lb);
-        vmul(a, l, a);
+        for (int s = 0; s < N; ++s)
 #pragma unroll
-        for (int i = 0; i < W; ++i) a[i] = ex2_fast(a[i]);
-        vset(b, 1.f);
+            for (int i = 0; i < W; ++i) a[s][i] = max_nan(a[s][i], least);
+#pragma unroll
+        for (int s = 0; s < N; ++s) vmul(a[s], rest, f[s]);
+#pragma unroll
+        for (int s = 0; s < N; ++s) vmul(a[s], head, a[s]);
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+#pragma unroll
+            for (int i = 0; i < W; ++i) a[s][i] = ex2_fast(a[s][i]);
+#pragma unroll
+        for (int s = 0; s < N; ++s) vfma(a[s], f[s], a[s], a[s]);
+#pragma unroll
+        for (int s = 0; s < N; ++s) vset(b[s], 1.f);
     } else {
 #pragma unroll
-        for (int i = 0; i < W; ++i) decay<T, SIG>(g[i], lb, a[i], b[i]);
+        for (int s = 0; s < N; ++s)
+#pragma unroll
+            for (int i = 0; i < W; ++i) decay<T, SIG>(a[s][i], lb, a[s][i], b[s][i]);
     }
+}
+template <typename T, bool SIG, int W> __device__ __forceinline__ void decays(const float (&g)[W], float lb, float (&a)[W], float (&b)[W]) {
+    float c[1][W], d[1][W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) c[0][i] = g[i];
+    decays<T, SIG, 1>(c, lb, d);
+#pragma unroll
+    for (int i = 0; i < W; ++i) a[i] = c[0][i], b[i] = d[0][i];
 }
 
 // State n's channels, or zeros.
@@ -242,29 +281,10 @@ __device__ __forceinline__ void steps_fwd(const R &ring, int slot, int s0, int r
     for (int s = 0; s < UN; ++s) ring.get(slot, 1, s0 + s, r + s, a[s]);
 #pragma unroll
     for (int s = 0; s < UN; ++s) ring.get(slot, 0, s0 + s, r + s, v[s]);
-    if constexpr (!SIG && sizeof(T) == 2) {
-        float l[W];
-        vset(l, kLog2e);
+    decays<T, SIG, UN>(a, lb, b);
+    if (SIG)
 #pragma unroll
-        for (int s = 0; s < UN; ++s)
-#pragma unroll
-            for (int i = 0; i < W; ++i) a[s][i] = max_nan(a[s][i], lb);
-#pragma unroll
-        for (int s = 0; s < UN; ++s) vmul(a[s], l, a[s]);
-#pragma unroll
-        for (int s = 0; s < UN; ++s)
-#pragma unroll
-            for (int i = 0; i < W; ++i) a[s][i] = ex2_fast(a[s][i]);
-    } else {
-#pragma unroll
-        for (int s = 0; s < UN; ++s) {
-            float g[W];
-#pragma unroll
-            for (int i = 0; i < W; ++i) g[i] = a[s][i];
-            decays<T, SIG>(g, lb, a[s], b[s]);
-            if (SIG) vmul(v[s], b[s], v[s]);
-        }
-    }
+        for (int s = 0; s < UN; ++s) vmul(v[s], b[s], v[s]);
 }
 
 template <typename T, int G, int LB, bool SIG>
