@@ -170,6 +170,15 @@ def _wanted(want_final, final_state_out):
         raise ValueError("final_state_out needs output_final_state")
 
 
+def _recorded(*tensors):
+    """Whether autograd records what is computed of the tensors (None: of none)."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
 def _no_outs(**outs):
     for name, t in outs.items():
         if t is not None:
@@ -292,7 +301,7 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, residual
     sum, s is the sum in x's dtype (written to ``residual_out`` if given, which may be
     ``residual`` or ``x`` itself). Gradients flow to x, weight, residual and gate.
     """
-    if torch.is_grad_enabled() and (x.requires_grad or any(t is not None and t.requires_grad for t in (weight, residual, gate))):
+    if _recorded(x, weight, residual, gate):
         _no_outs(out=out, residual_out=residual_out)
         return _RMSNorm.apply(x, weight, residual, gate, eps)
     return _rms_norm_fwd(x, weight, residual, gate, eps, out, residual_out)
@@ -308,7 +317,7 @@ def rms_norm_quant(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, re
     the scale max(max|y| / 448, 2^-100), with ``pow2_scales`` rounded up to a power of two.
     No gradients: inputs that require grad are refused.
     """
-    if torch.is_grad_enabled() and (x.requires_grad or any(t is not None and t.requires_grad for t in (weight, residual, gate))):
+    if _recorded(x, weight, residual, gate):
         raise NotImplementedError("rms_norm_quant has no gradients; use rms_norm")
     q, scales, s = _norm(x, weight, residual, gate, eps, residual_out, (group_size, pow2_scales, scales_out), out)
     return (q, scales) if residual is None else (q, scales, s)
@@ -406,7 +415,7 @@ def causal_conv(x: torch.Tensor, conv_w: torch.Tensor, *, initial_state: Optiona
     ``decode_token`` and ``causal_conv_step`` continue from the windows. Gradients flow to x,
     conv_w and initial_state.
     """
-    if torch.is_grad_enabled() and (x.requires_grad or conv_w.requires_grad or (initial_state is not None and initial_state.requires_grad)):
+    if _recorded(x, conv_w, initial_state):
         _no_outs(out=out, final_state_out=final_state_out)
         return _CausalConv.apply(x, conv_w, initial_state, output_final_state, cu_seqlens, cu_seqlens_cpu)
     return _causal_conv_fwd(x, conv_w, initial_state, output_final_state, cu_seqlens, cu_seqlens_cpu, out, final_state_out)[:2]
@@ -415,8 +424,11 @@ def causal_conv(x: torch.Tensor, conv_w: torch.Tensor, *, initial_state: Optiona
 def causal_conv_step(x: torch.Tensor, conv_w: torch.Tensor, conv_state: torch.Tensor, *,
                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One token of N sequences: x [N, C], conv_w [C, K] float32, conv_state [N, C, K] float32,
-    updated IN PLACE (shifted one slot, x last). Returns silu(w . window) [N, C].
+    updated IN PLACE (shifted one slot, x last). Returns silu(w . window) [N, C]. No gradients:
+    inputs and states that require grad are refused while gradients are recorded.
     """
+    if _recorded(x, conv_w, conv_state):
+        raise NotImplementedError("causal_conv_step has no gradients; use causal_conv")
     call = _abi.call("kda_causal_conv_step")
     dev = _dev("x", x)
     dt = _dtype("x", x)
@@ -535,7 +547,7 @@ def chunk_gated_scan(x: torch.Tensor, g: torch.Tensor, *, initial_state: Optiona
     Gradients flow to x, g and initial_state. A ``workspace`` passed in belongs to one call at
     a time (captured graphs that may overlap need one each).
     """
-    if torch.is_grad_enabled() and (x.requires_grad or g.requires_grad or (initial_state is not None and initial_state.requires_grad)):
+    if _recorded(x, g, initial_state):
         _no_outs(out=out, final_state_out=final_state_out, workspace=workspace)
         return _GatedScan.apply(x, g, initial_state, output_final_state, use_gate_sigmoid_in_kernel, lower_bound,
                                 cu_seqlens, cu_seqlens_cpu)
@@ -548,8 +560,11 @@ def gated_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *, us
                     state_out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One token of N sequences: x, g [N, D]; state [N, D] float32, updated IN PLACE, or only
     read when ``state_out`` (a second buffer, disjoint from it) receives the new state. Gate
-    arguments as in ``chunk_gated_scan``. Returns h [N, D].
+    arguments as in ``chunk_gated_scan``. Returns h [N, D]. No gradients: inputs and states that
+    require grad are refused while gradients are recorded.
     """
+    if _recorded(x, g, state, state_out):
+        raise NotImplementedError("gated_scan_step has no gradients; use chunk_gated_scan")
     call = _abi.call("kda_gated_scan_step")
     dev = _dev("x", x)
     dt = _dtype("x", x)
