@@ -5,7 +5,8 @@ As in `ops`, PyTorch supplies device memory and the current stream, and every st
 computation runs in the library's CUDA kernels. Activations may be slices of a fused
 projection: their channels have to be contiguous and their rows evenly spaced. Outputs are
 contiguous. Each function returns its gradients' counterpart through autograd where an input
-requires grad (the 8-bit norm and the single-token forms have none).
+requires grad (the 8-bit norm and the single-token forms have none). Tensors of the caller's that
+a call writes count as changed in place, so a backward pass that has saved one notices.
 """
 from __future__ import annotations
 
@@ -15,7 +16,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .ops import _DTYPES, _seqlens
+from .ops import _DTYPES, _seqlens, _written
 
 _F32 = _abi.KDA_DTYPE_F32
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device; what torch.cuda.current_stream wraps
@@ -236,6 +237,7 @@ def _norm(x, weight, residual, gate, eps, residual_out, quant=None, out=None):
     dt = _dtype("x", x)
     if x.dim() < 1:
         raise ValueError("x must be [..., D]")
+    given = [t for t in (out, residual_out, None if quant is None else quant[2]) if t is not None]
     D = x.shape[-1]
     wp, wdt = _weight(weight, x, dev)
     heads, ((xp, xs), (rp, rs), (gp, gs)) = _norm_rows((("x", x), ("residual", residual), ("gate", gate)), x, dev)
@@ -261,6 +263,8 @@ def _norm(x, weight, residual, gate, eps, residual_out, quant=None, out=None):
         scales = _out_as("scales_out", scales, shape, torch.float32, x.device, dev)
     _launch(call, call.pack(dt, wdt, x.numel() // D if D else 0, heads, D, xp, xs, rp, rs, gp, gs, wp, eps, y.data_ptr(),
                             _ptr(residual_out), _ptr(scales), group, int(pow2)), dev)
+    if given:
+        _written(*given)
     return y, scales, residual_out
 
 
@@ -377,6 +381,8 @@ def _causal_conv_fwd(x, conv_w, initial_state, want_final, cu_seqlens, cu_seqlen
     _wanted(want_final, final_state_out)
     fs = _out_as("final_state_out", final_state_out, (N, C, K), torch.float32, x.device, dev) if want_final else None
     _launch(call, call.pack(dt, B, T, C, K, xp, xs, conv_w.data_ptr(), s0, _ptr(fs), y.data_ptr(), _ptr(cu), _ptr(cu_host), N), dev)
+    if out is not None or final_state_out is not None:
+        _written(out, final_state_out)
     return y, fs, cu, cu_host
 
 
@@ -442,6 +448,7 @@ def causal_conv_step(x: torch.Tensor, conv_w: torch.Tensor, conv_state: torch.Te
     s = _state("conv_state", conv_state, (N, C, K), dev)
     y = _out("out", out, x, dev)
     _launch(call, call.pack(dt, N, C, K, xp, xs, conv_w.data_ptr(), s, y.data_ptr()), dev)
+    _written(conv_state, out)
     return y
 
 
@@ -505,6 +512,8 @@ def _gated_scan_fwd(x, g, initial_state, want_final, sigmoid, lower_bound, cu_se
     fs = _out_as("final_state_out", final_state_out, (N, D), torch.float32, x.device, dev) if want_final else None
     _launch_scratch(call, (dt, gate, B, T, D, xp, xs, gp, gs, h.data_ptr(), s0, _ptr(fs), _ptr(cu), _ptr(cu_host), N, has_lb, lb),
                     workspace, x.device, dev)
+    if out is not None or final_state_out is not None:
+        _written(out, final_state_out)
     return h, fs, cu, cu_host
 
 
@@ -579,6 +588,7 @@ def gated_scan_step(x: torch.Tensor, g: torch.Tensor, state: torch.Tensor, *, us
     s, so = _state("state", state, (N, D), dev), _state("state_out", state_out, (N, D), dev)
     h = _out("out", out, x, dev)
     _launch(call, call.pack(dt, gate, N, D, xp, xs, gp, gs, s, so, h.data_ptr(), has_lb, lb), dev)
+    _written(state if state_out is None else state_out, out)
     return h
 
 

@@ -12,6 +12,7 @@ import warnings
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _abi
 
@@ -27,6 +28,15 @@ def _need_cuda(name, t):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _written(*tensors):
+    """Raises the version of tensors of the caller's that a kernel writes (None: no tensor), as
+    PyTorch's own in-place operations do: a backward pass that has saved one then refuses to run
+    on what it has become."""
+    for t in tensors:
+        if t is not None:
+            increment_version(t)
 
 
 def _stream(device):
@@ -196,6 +206,8 @@ def _chunk_kda_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
         a.workspace_bytes = workspace.numel() * workspace.element_size()
     with torch.cuda.device(q.device):
         _abi.check(lib.kda_chunk_fwd(ctypes.byref(a), _stream(q.device)), "kda_chunk_fwd")
+    if out is not None or final_state_out is not None:
+        _written(out, final_state_out if output_final_state else None)
     return o, fs
 
 
@@ -276,6 +288,7 @@ def recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
                  use_beta_sigmoid_in_kernel)
     with torch.cuda.device(q.device):
         _abi.check(lib.kda_recurrent_step(ctypes.byref(a), _stream(q.device)), "kda_recurrent_step")
+    _written(state if state_out is None else state_out, out)
     return o
 
 
@@ -345,6 +358,7 @@ def decode_token(x: torch.Tensor, conv_w: torch.Tensor, conv_state: torch.Tensor
                  use_beta_sigmoid_in_kernel)
     with torch.cuda.device(x.device):
         _abi.check(lib.kda_decode_token(ctypes.byref(a), _stream(x.device)), "kda_decode_token")
+    _written(conv_state, state if state_out is None else state_out, out)
     return o
 
 

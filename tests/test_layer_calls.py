@@ -47,3 +47,82 @@ def test_steps_of_weights_that_are_trained_run_without_recording():
         with torch.no_grad():
             f(*leaf)
         assert not want[0].requires_grad
+
+
+# --------------------------------------------------------------------------- tensors that calls write
+
+@pytest.mark.gpu
+def test_written_tensors_count_as_changed():
+    """Each call raises the version of what it writes of the caller's, and of nothing else."""
+    import kimi_delta_attention_20_b200 as kda
+    H, D, K = 1, 32, 4
+    C = 3 * H * D
+
+    def z(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    x, w, g = z(2, 6, C), z(C, K), z(2, 6, C)
+    rows, q, k = z(2, C), z(2, H, D), z(1, 6, H, D)
+    beta, kbeta = z(2, H), z(1, 6, H)
+    calls = [  # function of the written tensors, those by name, and the tensors that are only read
+        (lambda out: kda.rms_norm(x, out=out), dict(out=z(2, 6, C)), [x]),
+        (lambda residual_out: kda.rms_norm(x, residual=g, residual_out=residual_out), dict(residual_out=z(2, 6, C)), [x, g]),
+        (lambda out, scales_out: kda.rms_norm_quant(x, out=out, scales_out=scales_out),
+         dict(out=z(2, 6, C, dtype=torch.float8_e4m3fn), scales_out=z(2, 6, 1)), [x]),
+        (lambda out, final_state_out: kda.causal_conv(x, w, out=out, final_state_out=final_state_out, output_final_state=True),
+         dict(out=z(2, 6, C), final_state_out=z(2, C, K)), [x, w]),
+        (lambda conv_state, out: kda.causal_conv_step(rows, w, conv_state, out=out), dict(conv_state=z(2, C, K), out=z(2, C)), [rows, w]),
+        (lambda out, final_state_out: kda.chunk_gated_scan(x, g, out=out, final_state_out=final_state_out, output_final_state=True),
+         dict(out=z(2, 6, C), final_state_out=z(2, C)), [x, g]),
+        (lambda state, out: kda.gated_scan_step(rows, rows, state, out=out), dict(state=z(2, C), out=z(2, C)), [rows]),
+        (lambda state_out, s=z(2, C): kda.gated_scan_step(rows, rows, s, state_out=state_out), dict(state_out=z(2, C)), [rows]),
+        (lambda conv_state, state, out: kda.decode_token(rows, w, conv_state, q, beta, state, out=out),
+         dict(conv_state=z(2, C, K), state=z(2, H, D, D), out=z(2, H, D)), [rows, w, q, beta]),
+        (lambda state, out: kda.recurrent_step(q, q, q, q, beta, state, out=out), dict(state=z(2, H, D, D), out=z(2, H, D)), [q, beta]),
+        (lambda state_out, s=z(2, H, D, D): kda.recurrent_step(q, q, q, q, beta, s, state_out=state_out), dict(state_out=z(2, H, D, D)), [q]),
+        (lambda out, final_state_out: kda.chunk_kda(k, k, k, k, kbeta, use_qk_l2norm_in_kernel=True, output_final_state=True, out=out,
+                                                    final_state_out=final_state_out), dict(out=z(1, 6, H, D), final_state_out=z(1, H, D, D)), [k, kbeta]),
+    ]
+    for i, (f, written, read) in enumerate(calls):
+        before, same = {n: t._version for n, t in written.items()}, [t._version for t in read]
+        f(**written)
+        assert all(t._version > before[n] for n, t in written.items()), i
+        assert [t._version for t in read] == same, i
+    state = z(2, C)
+    s = torch.zeros_like(state)
+    v = state._version
+    kda.gated_scan_step(rows, rows, state, state_out=s)
+    assert state._version == v  # only read
+    with torch.inference_mode():  # tensors that have no version
+        st = z(2, C)
+        kda.gated_scan_step(z(2, C), z(2, C), st, out=z(2, C))
+    kda.gated_scan_step(rows, rows, st)
+
+
+@pytest.mark.gpu
+def test_backward_notices_states_that_went_on():
+    """A window, state or term that a backward pass needs and a later call overwrites."""
+    import kimi_delta_attention_20_b200 as kda
+    H, D, K = 1, 32, 4
+    C = 3 * H * D
+
+    def rnd(*shape):
+        return torch.randn(*shape, generator=torch.Generator().manual_seed(sum(shape))).cuda()
+
+    x, w, g = rnd(2, 6, C).requires_grad_(), rnd(C, K), -rnd(2, 6, C).abs()
+    row, q, beta = rnd(2, C), rnd(2, H, D), rnd(2, H)
+    win, st, S, term = rnd(2, C, K), rnd(2, C), rnd(2, H, D, D), rnd(2, 6, C)
+    pairs = [
+        (lambda: kda.causal_conv(x, w, initial_state=win)[0], lambda: kda.causal_conv_step(row, w, win)),
+        (lambda: kda.causal_conv(x, w, initial_state=win)[0], lambda: kda.decode_token(row, w, win, -q.abs(), beta, S.clone())),
+        (lambda: kda.chunk_gated_scan(x, g, initial_state=st)[0], lambda: kda.gated_scan_step(row, row, st)),
+        (lambda: kda.chunk_gated_scan(x, g, initial_state=st)[0], lambda: kda.gated_scan_step(row, row, st.clone(), state_out=st)),
+        (lambda: x * term, lambda: kda.rms_norm(g, residual=term, residual_out=term)),
+        (lambda: x * term, lambda: kda.causal_conv(g, w, out=term)),
+    ]
+    for i, (forward, step) in enumerate(pairs):
+        forward().sum().backward()  # nothing in between
+        y = forward()
+        step()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
