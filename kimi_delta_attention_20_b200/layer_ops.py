@@ -5,8 +5,9 @@ As in `ops`, PyTorch supplies device memory and the current stream, and every st
 computation runs in the library's CUDA kernels. Activations may be slices of a fused
 projection: their channels have to be contiguous and their rows evenly spaced. Outputs are
 contiguous. Each function returns its gradients' counterpart through autograd where an input
-requires grad (the 8-bit norm and the single-token forms have none). Tensors of the caller's that
-a call writes count as changed in place, so a backward pass that has saved one notices.
+requires grad (the 8-bit norm and the single-token forms have none); forward-mode derivatives are
+refused. Tensors of the caller's that a call writes count as changed in place, so a backward pass
+that has saved one notices.
 """
 from __future__ import annotations
 
@@ -16,7 +17,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _abi
-from .ops import _DTYPES, _seqlens, _written
+from .ops import _DTYPES, _no_tangents, _seqlens, _written
 
 _F32 = _abi.KDA_DTYPE_F32
 _raw_stream = torch._C._cuda_getCurrentRawStream  # of a device; what torch.cuda.current_stream wraps
@@ -173,6 +174,7 @@ def _wanted(want_final, final_state_out):
 
 def _recorded(*tensors):
     """Whether autograd records what is computed of the tensors (None: of none)."""
+    _no_tangents(*tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
@@ -334,6 +336,7 @@ def rms_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: Optional[torch.Tenso
     of y. x is what was normed: with a residual, the sum s that the forward returned; dx is
     then the gradient of both terms, and ``dresidual``, the cotangent of s, is added to it.
     """
+    _no_tangents(x, dy, weight, gate, dresidual)
     call = _abi.call("kda_rms_norm_bwd")
     dev = _dev("x", x)
     dt = _dtype("x", x)
@@ -461,6 +464,7 @@ def causal_conv_bwd(x: torch.Tensor, conv_w: torch.Tensor, dy: torch.Tensor, *,
     cotangents ``dy`` of y and, optionally, ``dfinal_state`` [N, C, K] float32 of the final
     windows. dinitial_state comes with an initial_state unless asked for otherwise.
     """
+    _no_tangents(x, conv_w, dy, initial_state, dfinal_state)
     call = _abi.call("kda_causal_conv_bwd")
     dev = _dev("x", x)
     dt = _dtype("x", x)
@@ -603,6 +607,7 @@ def chunk_gated_scan_bwd(x: Optional[torch.Tensor], g: torch.Tensor, h: torch.Te
     the lower bound is taken (g < lower_bound). dinitial_state comes with an initial_state
     unless asked for otherwise.
     """
+    _no_tangents(x, g, h, dout, initial_state, dfinal_state)
     call = _abi.call("kda_gated_scan_bwd")
     dev = _dev("g", g)
     dt = _dtype("g", g)

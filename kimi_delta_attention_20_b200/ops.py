@@ -12,6 +12,7 @@ import warnings
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.graph import increment_version
 
 from . import _abi
@@ -28,6 +29,15 @@ def _need_cuda(name, t):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _no_tangents(*tensors):
+    """Refuses tensors (None: no tensor) that carry forward-mode derivatives: no function here
+    has any, and their outputs would come without."""
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("forward-mode derivatives are not provided")
 
 
 def _written(*tensors):
@@ -146,6 +156,7 @@ def _chunk_kda_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     call is recorded for the backward (``chunk_kda_bwd``): gradients flow to
     those inputs (the log-decay form; in-kernel gate forms raise).
     """
+    _no_tangents(q, k, v, g, beta, A_log, dt_bias, initial_state)
     lib = _abi.load()
     for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta)):
         _need_cuda(name, t)
@@ -264,6 +275,7 @@ def recurrent_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.T
     buffer, disjoint from ``state``) receives the new state. Gate arguments as in
     ``chunk_kda``. Returns o [N, H, Dv].
     """
+    _no_tangents(q, k, v, g, beta, state, A_log, dt_bias)
     lib = _abi.load()
     for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("state", state)):
         _need_cuda(name, t)
@@ -313,6 +325,7 @@ def decode_token(x: torch.Tensor, conv_w: torch.Tensor, conv_state: torch.Tensor
     arguments as in ``recurrent_step``. Returns o [N, H, Dv]: the gated, normalised
     output with ``g_out``, else the recurrent step's output.
     """
+    _no_tangents(x, conv_w, conv_state, g, beta, state, g_out, A_log, dt_bias)
     lib = _abi.load()
     for name, t in (("x", x), ("conv_w", conv_w), ("conv_state", conv_state), ("g", g), ("beta", beta),
                     ("state", state)):
@@ -377,6 +390,7 @@ def chunk_kda_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     the dtype of q, dinitial_state is fp32. The gradient of g is zero where the
     lower bound is taken (g < lower_bound).
     """
+    _no_tangents(q, k, v, g, beta, dout, dfinal_state, initial_state)
     lib = _abi.load()
     for name, t in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("dout", dout)):
         _need_cuda(name, t)

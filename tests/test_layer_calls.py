@@ -49,6 +49,46 @@ def test_steps_of_weights_that_are_trained_run_without_recording():
         assert not want[0].requires_grad
 
 
+def tangent_calls(dev):
+    """Every function with the tensors that it reads."""
+    import kimi_delta_attention_20_b200 as kda
+
+    def z(*shape):
+        return torch.zeros(shape, device=dev)
+
+    H, D, K = 1, 32, 4
+    C = 3 * H * D
+    x, w, cw, win, st, S, beta = z(2, 6, C), z(C), z(C, K), z(2, C, K), z(2, C), z(2, H, D, D), z(2, 6, H)
+    q, t = z(2, 6, H, D), z(2, H, D)
+    return [
+        (lambda a, b, c: kda.rms_norm(a, b, residual=c), [x, w, x]), (lambda a, b, c: kda.rms_norm(a, b, gate=c), [x, w, x]),
+        (lambda a, b, c: kda.rms_norm_quant(a, b, residual=c), [x, w, x]), (lambda a, b, c, d: kda.rms_norm_bwd(a, b, c, gate=d), [x, x, w, x]),
+        (lambda a, b, c: kda.rms_norm_bwd(a, b, dresidual=c), [x, x, x]),
+        (lambda a, b, c: kda.causal_conv(a, b, initial_state=c), [x, cw, win]), (kda.causal_conv_step, [x[:, 0], cw, win]),
+        (lambda a, b, c, d, e: kda.causal_conv_bwd(a, b, c, initial_state=d, dfinal_state=e), [x, cw, x, win, win]),
+        (lambda a, b, c: kda.chunk_gated_scan(a, b, initial_state=c), [x, x, st]), (kda.gated_scan_step, [x[:, 0], x[:, 0], st]),
+        (lambda a, b, c, d, e: kda.chunk_gated_scan_bwd(None, a, b, c, initial_state=d, dfinal_state=e), [x, x, x, st, st]),
+        (lambda a, b, c, d, e, f: kda.chunk_kda(a, b, c, d, e, initial_state=f, use_qk_l2norm_in_kernel=True), [q, q, q, q, beta, S]),
+        (kda.recurrent_step, [t, t, t, t, beta[:, 0], S]), (kda.decode_token, [x[:, 0].contiguous(), cw, win, t, beta[:, 0].contiguous(), S]),
+        (lambda a, b, c, d, e, f, g: kda.chunk_kda_bwd(a, b, c, d, e, f, dfinal_state=g), [q, q, q, q, beta, q, S]),
+    ]
+
+
+def test_forward_mode_derivatives_are_refused():
+    """A tangent on any input, which the outputs could not carry on; within a dual level, calls
+    without tangents are what they were."""
+    from torch.autograd import forward_ad
+    with forward_ad.dual_level():
+        for i, (f, args) in enumerate(tangent_calls("cpu")):
+            for k in range(len(args)):
+                dual = [forward_ad.make_dual(a, torch.ones_like(a)) if j == k else a for j, a in enumerate(args)]
+                with pytest.raises(NotImplementedError):
+                    f(*dual)
+                    print("not refused:", i, k)
+            with pytest.raises(ValueError):  # on the CPU
+                f(*args)
+
+
 # --------------------------------------------------------------------------- tensors that calls write
 
 @pytest.mark.gpu
