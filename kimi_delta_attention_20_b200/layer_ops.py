@@ -20,7 +20,8 @@ from . import _abi
 from .ops import _DTYPES, _no_tangents, _seqlens, _written
 
 _F32 = _abi.KDA_DTYPE_F32
-_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device; what torch.cuda.current_stream wraps
+# of a device; what torch.cuda.current_stream wraps (a torch without CUDA has none, and no tensors to launch on)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _dev(name, t):

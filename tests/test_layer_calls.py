@@ -1,11 +1,16 @@
 """Calls of the operators around the state update that are refused, or whose side effects
 autograd has to see: host-side checks, and the same on the GPU where a launch is needed."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 from kimi_delta_attention_20_b200 import _abi
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 A, B, C, D_ = (0x1000000 * (k + 1) for k in range(4))  # far apart, never dereferenced
 
@@ -166,3 +171,17 @@ def test_backward_notices_states_that_went_on():
         step()
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.sum().backward()
+
+
+# --------------------------------------------------------------------------- import
+
+def test_import_on_a_torch_without_cuda():
+    """The binding loads where PyTorch was built without CUDA, and its functions then refuse
+    their tensors by name."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, n)\n"
+            "import kimi_delta_attention_20_b200 as kda\n"
+            "try: kda.rms_norm(torch.zeros(2, 8))\n"
+            "except ValueError as e: print('refused:', e)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "refused: x must be a CUDA tensor", r.stderr
