@@ -25,11 +25,6 @@ constexpr int kFwdStages = 6, kBwdStages = 3;
 template <typename T, int G> using FwdRing = Ring<T, G, kLB, kStage, 1, kFwdStages>;
 template <typename T, int G> using BwdRing = Ring<T, G, kLB, kStage, 2, kBwdStages>;
 
-// sigmoid, by the SFU where the result is rounded to bf16.
-template <typename T> __device__ __forceinline__ float sig(float z) {
-    return sizeof(T) == 2 ? rcp_fast(1.f + ex2_fast(-kLog2e * z)) : 1.f / (1.f + expf(-z));
-}
-
 // The lane's weights: w[c, 0..K-1] of its channels.
 template <int K, int W> __device__ __forceinline__ void load_weights(const float *w, int c, int C, float (&wr)[K][W]) {
 #pragma unroll
@@ -360,19 +355,11 @@ int piece_rows(int rows, int C, bool bf16) {
 }
 int pieces_of(int rows, int piece) { return rows > piece ? (int)(((long long)rows + piece - 1) / piece) : 1; }
 
-template <typename T, typename P> cudaError_t run_walk(void (*kernel)(P), const P &p, int ring_bytes, cudaStream_t st) {
-    const long long grid = (long long)p.pieces * units_of(p.C, sizeof(T) == 2);
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    count_launch();
-    kernel<<<(unsigned)grid, 32, ring_bytes, st>>>(p);
-    return cudaGetLastError();
-}
-
 template <typename T, int G, int K> cudaError_t run_fwd(const ConvParams &p, cudaStream_t st) {
-    return run_walk<T>(conv_fwd_kernel<T, G, K>, p, FwdRing<T, G>::BYTES, st);
+    return run_walk(conv_fwd_kernel<T, G, K>, p, p.pieces, units_of(p.C, sizeof(T) == 2), FwdRing<T, G>::BYTES, st);
 }
 template <typename T, int G, int K> cudaError_t run_bwd(const ConvBwdParams &p, cudaStream_t st) {
-    const cudaError_t e = run_walk<T>(conv_bwd_kernel<T, G, K>, p, BwdRing<T, G>::BYTES, st);
+    const cudaError_t e = run_walk(conv_bwd_kernel<T, G, K>, p, p.pieces, units_of(p.C, sizeof(T) == 2), BwdRing<T, G>::BYTES, st);
     if (e != cudaSuccess || !p.dw) return e;
     return launch_next_pass(conv_dw_kernel, (unsigned)(((long long)p.C * K + 31) / 32), 1024, st, (const float *)p.partial, p.dw, p.pieces, p.C, K);
 }

@@ -103,11 +103,6 @@ template <typename T, int G> __device__ __forceinline__ void load_weight(const v
     }
 }
 
-// sigmoid, by the SFU where the result is rounded to bf16 (2 + 1 steps off).
-template <typename T> __device__ __forceinline__ float sig(float x) {
-    return sizeof(T) == 2 ? rcp_fast(1.f + ex2_fast(-kLog2e * x)) : 1.f / (1.f + expf(-x));
-}
-
 template <int TPR> constexpr int norm_threads() { return TPR > 128 ? TPR : 128; }
 // Floats that a reduction over rows that span warps needs.
 template <int TPR> constexpr int norm_red() { return TPR > 32 ? norm_threads<TPR>() / 32 : 1; }

@@ -152,7 +152,7 @@ __device__ __forceinline__ int piece_of(const ScanCut &cut, const RowSpan &sp, i
 
 // A lane's channels of a piece's map: A and H of each, W pairs side by side. A map where a
 // sequence begins leaves nothing of what came before, not even as 0 x inf: its A is below 0.
-template <int W> struct __align__(W == 1 ? 8 : 16) Map {
+template <int W> struct __align__(16) Map {
     float2 ch[W];
 };
 
@@ -176,10 +176,7 @@ __device__ __forceinline__ void compose(const Map<W> *at, long long pitch, int f
             if (u < n) {
                 const float4 *q = reinterpret_cast<const float4 *>(at + (long long)(k + u * step) * pitch);
 #pragma unroll
-                for (int j = 0; j < (W + 1) / 2; ++j) {
-                    if constexpr (W == 1) m[u].ch[0] = *reinterpret_cast<const float2 *>(q);
-                    else reinterpret_cast<float4 *>(m[u].ch)[j] = q[j];
-                }
+                for (int j = 0; j < W / 2; ++j) reinterpret_cast<float4 *>(m[u].ch)[j] = q[j];
             }
 #pragma unroll
         for (int u = 0; u < BATCH; ++u)
@@ -242,15 +239,8 @@ __global__ void __launch_bounds__(1024) scan_carry_kernel(const void *maps, floa
     }
 }
 
-// The state before (backward: behind) a piece, from the carry kernel or composed here of the
-// maps from piece `first` on. Without maps (a cut after the host's offsets, none of which the
-// device's may share) zeros.
 template <int W>
-__device__ __forceinline__ void enter(const ScanCut &cut, int c0, int units, int first, int piece, int step, float (&c)[W]) {
-    if (!cut.maps) {
-        vset(c, 0.f);
-        return;
-    }
+__device__ __forceinline__ void enter_cut(const ScanCut &cut, int c0, int units, int first, int piece, int step, float (&c)[W]) {
     if (!cut.carry) {
         compose(lane_map<W>(cut, c0), (long long)units * 32, first, piece, step, c);
         return;
@@ -259,7 +249,19 @@ __device__ __forceinline__ void enter(const ScanCut &cut, int c0, int units, int
 #pragma unroll
     for (int i = 0; i < W; ++i) c[i] = p[i];
 }
-
+// The state before (backward: behind) a piece, from the carry kernel or composed here of the
+// maps from piece `first` on. Without maps (a cut after the host's offsets, none of which the
+// device's may share) zeros; lanes of 4 bytes never have any.
+template <int LB, int W>
+__device__ __forceinline__ void enter(const ScanCut &cut, int c0, int units, int first, int piece, int step, float (&c)[W]) {
+    if constexpr (LB == 8) {
+        if (cut.maps) {
+            enter_cut(cut, c0, units, first, piece, step, c);
+            return;
+        }
+    }
+    vset(c, 0.f);
+}
 // ---------------------------------------------------------------- forward
 // One step of a lane's channels: a, and what is added to a h.
 template <typename T, bool SIG, typename R, int W>
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(32) scan_fwd_kernel(const __grid_constant__ Sc
     if (b >= e) return;
     Seq q = seq_of(p.span, b, lane);
     float h[W];
-    if (q.start < b) enter(p.cut, c, units, piece_of(p.cut, p.span, q.start), piece, 1, h);
+    if (q.start < b) enter<LB>(p.cut, c, units, piece_of(p.cut, p.span, q.start), piece, 1, h);
     else get_state(p.s0, q.n, c, D, h);
     // behind the last row of a sequence
     auto close = [&](int row) {
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(32) scan_bwd_kernel(const __grid_constant__ Sc
     if (b >= e) return;
     Seq q = seq_of(p.span, e - 1, lane);
     float k[W];
-    if (q.end > e) enter(p.cut, c, units, piece_of(p.cut, p.span, q.end - 1), piece, -1, k);
+    if (q.end > e) enter<LB>(p.cut, c, units, piece_of(p.cut, p.span, q.end - 1), piece, -1, k);
     else get_state(p.dsT, q.n, c, D, k);
     int slot = 0, next = ST - 1;
 #pragma unroll 1
@@ -730,15 +732,6 @@ ScanCut scan_cut(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, in
     return narrow.carries ? wide : narrow;
 }
 
-// Launches a walker for each piece and channel unit.
-template <typename T, typename P> cudaError_t run_walk(void (*kernel)(P), const P &p, int ring_bytes, cudaStream_t st) {
-    const long long grid = (long long)p.cut.pieces * units_of(p.D, sizeof(T) == 2, p.cut.lb);
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    count_launch();
-    kernel<<<(unsigned)grid, 32, ring_bytes, st>>>(p);
-    return cudaGetLastError();
-}
-
 template <int W> cudaError_t run_carry(const ScanCut &c, int D, bool bf16, int backward, cudaStream_t st) {
     if (!c.carry) return cudaSuccess;
     const int units = units_of(D, bf16, c.lb);
@@ -750,20 +743,22 @@ template <int W> cudaError_t run_carry(const ScanCut &c, int D, bool bf16, int b
 // Lanes of 4 bytes come with one pass over the rows and wide accesses (see scan_cut).
 template <typename T, int G, int LB, bool SIG> cudaError_t run_fwd_lb(const ScanParams &p, cudaStream_t st) {
     constexpr int ring = ScanRing<T, G, LB, 2>::BYTES;
+    const int units = units_of(p.D, sizeof(T) == 2, LB);
     cudaError_t e = cudaSuccess;
     if constexpr (LB == 8) {
-        if (p.cut.carries) e = run_walk<T>(scan_reduce_kernel<T, G, LB, SIG>, p, ring, st);
+        if (p.cut.carries) e = run_walk(scan_reduce_kernel<T, G, LB, SIG>, p, p.cut.pieces, units, ring, st);
         if (e == cudaSuccess) e = run_carry<lane_channels<T, LB>()>(p.cut, p.D, sizeof(T) == 2, 0, st);
     }
-    return e != cudaSuccess ? e : run_walk<T>(scan_fwd_kernel<T, G, LB, SIG>, p, ring, st);
+    return e != cudaSuccess ? e : run_walk(scan_fwd_kernel<T, G, LB, SIG>, p, p.cut.pieces, units, ring, st);
 }
 template <typename T, int G, int LB, bool SIG> cudaError_t run_bwd_lb(const ScanBwdParams &p, cudaStream_t st) {
+    const int units = units_of(p.D, sizeof(T) == 2, LB);
     cudaError_t e = cudaSuccess;
     if constexpr (LB == 8) {
-        if (p.cut.carries) e = run_walk<T>(scan_reduce_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, 2>::BYTES, st);
+        if (p.cut.carries) e = run_walk(scan_reduce_bwd_kernel<T, G, LB, SIG>, p, p.cut.pieces, units, ScanRing<T, G, LB, 2>::BYTES, st);
         if (e == cudaSuccess) e = run_carry<lane_channels<T, LB>()>(p.cut, p.D, sizeof(T) == 2, 1, st);
     }
-    return e != cudaSuccess ? e : run_walk<T>(scan_bwd_kernel<T, G, LB, SIG>, p, ScanRing<T, G, LB, SIG ? 4 : 3>::BYTES, st);
+    return e != cudaSuccess ? e : run_walk(scan_bwd_kernel<T, G, LB, SIG>, p, p.cut.pieces, units, ScanRing<T, G, LB, SIG ? 4 : 3>::BYTES, st);
 }
 template <typename T, int G, bool SIG> cudaError_t run_fwd(const ScanParams &p, cudaStream_t st) {
     if constexpr (G >= 8)

@@ -50,6 +50,15 @@ cudaError_t launch_next_pass(void (*kernel)(P...), unsigned grid, unsigned threa
     return e != cudaSuccess ? cudaGetLastError() : e;
 }
 
+// Launches a walker, one warp, for each piece and channel unit.
+template <typename P> cudaError_t run_walk(void (*kernel)(P), const P &p, int pieces, int units, int ring_bytes, cudaStream_t st) {
+    const long long grid = (long long)pieces * units;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    count_launch();
+    kernel<<<(unsigned)grid, 32, ring_bytes, st>>>(p);
+    return cudaGetLastError();
+}
+
 // ---------------------------------------------------------------- arithmetic
 // The SFU's exponential (off by 2 steps) and reciprocal (1 step), for bf16 results.
 __device__ __forceinline__ float ex2_fast(float x) {
@@ -63,6 +72,10 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return r;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+// sigmoid, by the SFU where the result is rounded to bf16 (2 + 1 steps off).
+template <typename T> __device__ __forceinline__ float sig(float x) {
+    return sizeof(T) == 2 ? rcp_fast(1.f + ex2_fast(-kLog2e * x)) : 1.f / (1.f + expf(-x));
+}
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
