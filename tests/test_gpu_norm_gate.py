@@ -10,7 +10,7 @@ DEV = "cuda"
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("M,D", [(5, 64), (7, 1023), (700, 512), (2000, 128)])
+@pytest.mark.parametrize("M,D", [(5, 64), (7, 1023), (700, 512), (2000, 128), (4, 7000), (650, 5003), (3, 16384)])
 def test_gradients_of_saturated_gates(M, D, dtype):
     """dgate = dy x r w p (1 - p) falls like exp(-|gate|) on both sides, and holds its digits there."""
     import kimi_delta_attention_20_b200 as kda
@@ -33,10 +33,11 @@ def test_gradients_of_saturated_gates(M, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_gates_at_the_ends(dtype):
+@pytest.mark.parametrize("D", [96, 5000])
+def test_gates_at_the_ends(D, dtype):
     """Infinite gates are open or shut for good; a NaN stays in its row."""
     import kimi_delta_attention_20_b200 as kda
-    x = torch.randn(4, 96, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(dtype)
+    x = torch.randn(4, D, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(dtype)
     gate = torch.zeros_like(x)
     gate[0], gate[1], gate[2, 5] = float("inf"), float("-inf"), float("nan")
     dx, dgate, _ = kda.rms_norm_bwd(x, x, gate=gate)
