@@ -5,9 +5,11 @@
 // where a sequence's inputs are preceded by its initial window (K values a channel, oldest
 // first, or zeros), and its final window is the last K of both.
 //
-// 4 bytes an element forward, 6 backward (bf16), but bound by the special-function unit, which
-// takes two instructions an element and is 61 % busy, and in the backward by issue: 8192 x 6144
-// in 41 us (4.9 TB/s), 65536 x 1024 backward in 85 us (4.7 TB/s). A walker slides the window
+// 4 bytes an element forward, 6 backward (bf16). 8192 x 6144, ragged with windows, takes 43 us a
+// call (4.7 TB/s) where its bytes take 31 and its two special-function instructions an element
+// 25: neither is full (59 % of that pipe, 48 % of issue), the walkers of an SM do not overlap
+// them any better. 65536 x 1024 backward takes 92 us (4.4 TB/s) with 57 % of issue and 38 % of that
+// pipe: latency, with 13 of its warps an SM at 126 registers. A walker slides the window
 // down its piece of the rows in registers. Nothing is carried between pieces but K - 1
 // rows that are read twice, so pieces are cut for full waves of walkers: sixteen an SM with
 // rings of 12 KiB, since they need the arithmetic of many warps beside the bytes in flight

@@ -8,10 +8,11 @@
 //     dgate = dy s r w sigmoid'(gate),  dw = sum over rows of dy s r sigmoid(gate)
 //
 // Bound by HBM: every tensor passes once, the row stays in registers between the sum of
-// squares and the output (786432 x 128 gated 97 us, 6.2 TB/s; 16384 x 4096 with residual to 8
-// bits 87 us, 5.4 TB/s, where conversions take issue too). A row belongs to TPR threads (part of a warp for heads, up to a
-// CTA for layers), each with NU runs of eight channels. The sum x + residual is rounded
-// to its type for `residual_out` alone: the norm is taken of the fp32 sum.
+// squares and the output (786432 x 128 gated 105 us a call, 5.8 TB/s; 16384 x 4096 with residual
+// to 8 bits 92 us, 5.1 TB/s, where conversions and the quotient's rounding take issue too, 61 %
+// of the slots). A row belongs to TPR threads (part of a warp for heads, up to a CTA for
+// layers), each with NU runs of eight channels. The sum x + residual is rounded to its type for
+// `residual_out` alone: the norm is taken of the fp32 sum.
 #pragma once
 
 #include <cuda_fp8.h>

@@ -5,8 +5,8 @@
 //
 // 6 bytes an element forward, 10 backward (bf16; 12 in the sigmoid form). Bound by HBM where
 // walkers are many, by the instructions of one warp along the longest sequence (41 ns a row)
-// where they just fill the GPU: 31744 x 12288 in four sequences 509 us (4.6 TB/s); and by the
-// second reading where time is cut: 8192 x 2048 backward, sigmoid form, 46 us (4.4 TB/s).
+// where they just fill the GPU: 31744 x 12288 in four sequences 502 us a call (4.7 TB/s); and by
+// the second reading where time is cut: 8192 x 2048 backward, sigmoid form, 50 us (4.0 TB/s).
 // Each element is read once, decayed once and written once by a walker, which carries the
 // states of its channels in registers; seven walkers share an SM, and nothing waits for
 // another CTA.
@@ -16,10 +16,12 @@
 // from zero; a sequence's first row drops what came before): a first kernel reduces each
 // piece to its map, and the walker of a piece composes the maps of the pieces before it,
 // back to where its sequence began, before it starts. That reads two of the tensors a second
-// time, from L2 where they fit. Handing states from CTA to CTA inside one kernel would read
+// time. A forward whose inputs fit L2 finds them there (8192 x 2048: 7 of 67 MB come from DRAM);
+// larger ones do not (131072 x 257 fp32: 273 of 270 MB), nor does the backward, whose second pass
+// streams its other tensors over them (8192 x 2048: it reads 117 of 134 MB). Handing states from CTA to CTA inside one kernel would read
 // once, but measured slower: links of a chain have to wait for one another, and every row is
 // walked twice by the CTA that holds it (31744 x 12288: 768 us; 8192 x 2048 backward: 82
-// against 47; with flags behind fences a handover alone took 8 us under load). What is
+// against 47 then; with flags behind fences a handover alone took 8 us under load). What is
 // composed, and in which order, goes by the shapes: results do not depend on timing.
 #include <type_traits>
 
@@ -275,7 +277,7 @@ __device__ __forceinline__ void step_fwd(const R &ring, int slot, int s, int r, 
 
 // The same of rows s0 .. s0+UN-1 of a stage, one operation of all of them after the other: a
 // walker has its scheduler almost to itself, so neighbouring instructions have to be
-// independent (31744 x 12288: 502 us; 529 row after row).
+// independent (31744 x 12288: 5 % of the call's time).
 template <typename T, bool SIG, int UN, typename R, int W>
 __device__ __forceinline__ void steps_fwd(const R &ring, int slot, int s0, int r, float lb, float (&a)[UN][W], float (&v)[UN][W]) {
     float b[UN][W];
@@ -665,7 +667,14 @@ int pieces_of(int rows, int each) { return (int)(((long long)rows + each - 1) / 
 // whole sequences come to half of those that can run at a time, none more than three times
 // as long as the average (one pass; without the lengths on the host a packed batch is taken
 // to be ragged); otherwise pieces of equal length, for one full wave of walkers and of
-// kMinPiece rows at least.
+// kMinPiece rows at least. Forward and backward (log form) of 2048 channels in bf16, where 64 pieces are
+// a wave, us, whole against cut:
+//   32 x 1024 rows 62, 106 against 78, 134;  31 x 1024 60, 105 against 76, 127 (cut, the far side of
+//   the rule);  16 x 1024 58, 102 against 51, 76: the two sides meet between a quarter and half
+//   32 packed of 1000 rows on average, longest 1000: 62, 106 against 97, 155;  2000: 114, 199
+//   against 101, 152 (whole);  3000: 168, 296 against 100, 152
+//   64 packed, longest 2000: 157, 273 against 188, 284;  3000: 204, 363 against 192, 287
+//   512 packed of 128 rows 125, 211 against 146, 248 (cut: more than four waves)
 ScanCut cut_for(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int lb) {
     const int units = units_of(D, bf16, lb);
     const long long want = kWalkerSlots > units ? kWalkerSlots / units : 1;  // pieces of a full wave
@@ -709,8 +718,8 @@ ScanCut cut_for(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int
 }
 
 // A walker composes up to this many maps itself; beyond, a kernel between the two passes
-// hands every walker its state: it takes 7 us, which 64 pieces do not repay (8192 x 2048
-// backward: 48 us without, 55 with it) and 518 do (131072 x 256 in bf16: 105 without, 85).
+// hands every walker its state. Forward of bf16, us, without it and with it: 129 pieces 64 and
+// 67, 207 and 259 the same, 345 pieces 109 and 105, 518 pieces 104 and 87, 1036 pieces 106 and 65.
 constexpr int kOwnMaps = 256;
 
 // Scratch: the maps, then the states before the pieces.
@@ -724,7 +733,9 @@ void lay_out(ScanCut *c, int D, bool bf16, void *workspace) {
 // Lanes of 8 bytes take about two thirds of the instructions an element; lanes of 4 make
 // twice the walkers, and are taken where they save the cut along time (31744 x 12288 packed
 // of four sequences: 511 us in one pass, 637 with lanes of 8 in two; x 12292, by 8 bytes: 859
-// against 996), but for accesses of less than 8 bytes (x 12289: 2017 against 1021).
+// against 996), but for accesses of less than 8 bytes (x 12289: 2017 against 1021). At the least
+// number of walkers that take them, 16 x 1024 x 2048, the forward gains (41 against 51) and the
+// backward loses (88 against 76).
 ScanCut scan_cut(const RowSpan &sp, const int32_t *cu_host, int D, bool bf16, int g) {
     const ScanCut wide = cut_for(sp, cu_host, D, bf16, 8);
     if (!wide.carries || g < 8) return wide;
