@@ -366,7 +366,9 @@ KDA_API kda_status kda_chunk_fwd_noalloc_status(const kda_chunk_args *args, void
  *    trusted (it moves no access out of the buffers, whatever it holds).
  *  - An output or workspace that overlaps an input or another output is refused,
  *    except where stated.
- *  - Sums, norms, states and convolution windows are fp32.
+ *  - Sums, norms, states and convolution windows are fp32. Of bf16 inputs exponentials
+ *    and sigmoids come from the special-function unit, a few 2^-24 off (a decay of the
+ *    scan's log form at most 7), which fp32 outputs show too; of fp32 inputs from expf.
  */
 
 /*

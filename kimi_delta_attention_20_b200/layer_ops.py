@@ -14,6 +14,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _abi
@@ -175,7 +176,8 @@ def _wanted(want_final, final_state_out):
 
 def _recorded(*tensors):
     """Whether autograd records what is computed of the tensors (None: of none)."""
-    _no_tangents(*tensors)
+    if forward_ad._current_level >= 0:
+        _no_tangents(*tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
